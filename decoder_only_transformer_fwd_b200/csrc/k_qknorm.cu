@@ -1,0 +1,317 @@
+// QK-norm with RoPE at given positions, written to a dense output or into cache
+// rows, and its gradient.
+//
+// "The Mathematics of Karpathy's nanochat", §QK-Norm with Sharpening, §Rotary
+// Position Embeddings: with R(t) the half-split rotation by t theta_i,
+// theta_i = base^(-2i/D),
+//   y = alpha R x / rho,   rho = sqrt(mean(x^2) + eps)
+// (the rotation keeps the norm, so rho is taken from x).  Its gradient, with
+// b = R^T dy,
+//   dx = (alpha / rho) (b - x (x . b) / (D rho^2)).
+//
+// Both passes only move data: (H + 2 H_kv) D elements per token in and out
+// (forward), 2 (H + H_kv) D in and (H + H_kv) D out (backward).
+#include "nc_internal.cuh"
+
+namespace nc {
+
+namespace {
+
+constexpr int kD = 128, kHalf = 64;
+constexpr int kThreads = 256;
+
+struct RopeFreq {
+  // theta_i / 2 pi as a fraction of 2^64: position * turns mod 2^64 is the
+  // phase in turns, exact in integers for every 31-bit position
+  unsigned long long turns[kHalf];
+};
+
+struct Vec {  // one lane's part of a head vector: dims [8 j, 8 j + 8) and [64 + 8 j, 64 + 8 j + 8)
+  float a[8], b[8];
+};
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<uint32_t*>(&v);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T> struct Raw;  // the untouched 16-byte words of a Vec
+template <> struct Raw<bf16> {
+  uint4 w[2];
+  __device__ __forceinline__ void load(const bf16* p, int j) {
+    w[0] = *reinterpret_cast<const uint4*>(p + 8 * j);
+    w[1] = *reinterpret_cast<const uint4*>(p + kHalf + 8 * j);
+  }
+  __device__ __forceinline__ void store(bf16* p, int j) const {
+    *reinterpret_cast<uint4*>(p + 8 * j) = w[0];
+    *reinterpret_cast<uint4*>(p + kHalf + 8 * j) = w[1];
+  }
+  __device__ __forceinline__ Vec get() const {
+    Vec v;
+    unpack8(w[0], v.a);
+    unpack8(w[1], v.b);
+    return v;
+  }
+  __device__ __forceinline__ void set(const Vec& v) {
+    w[0] = pack8(v.a);
+    w[1] = pack8(v.b);
+  }
+};
+template <> struct Raw<float> {
+  float4 w[4];
+  __device__ __forceinline__ void load(const float* p, int j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(p + (i >> 1) * kHalf + 8 * j + 4 * (i & 1));
+  }
+  __device__ __forceinline__ void store(float* p, int j) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(p + (i >> 1) * kHalf + 8 * j + 4 * (i & 1)) = w[i];
+  }
+  __device__ __forceinline__ Vec get() const {
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v.a[4 * i] = w[i].x, v.a[4 * i + 1] = w[i].y, v.a[4 * i + 2] = w[i].z, v.a[4 * i + 3] = w[i].w;
+      v.b[4 * i] = w[2 + i].x, v.b[4 * i + 1] = w[2 + i].y, v.b[4 * i + 2] = w[2 + i].z, v.b[4 * i + 3] = w[2 + i].w;
+    }
+    return v;
+  }
+  __device__ __forceinline__ void set(const Vec& v) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = make_float4(v.a[4 * i], v.a[4 * i + 1], v.a[4 * i + 2], v.a[4 * i + 3]);
+      w[2 + i] = make_float4(v.b[4 * i], v.b[4 * i + 1], v.b[4 * i + 2], v.b[4 * i + 3]);
+    }
+  }
+};
+
+// sum over the eight lanes that share a head vector
+__device__ __forceinline__ float sum8(float v, unsigned mask) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+  return v;
+}
+
+// cos and sin of a position's 64 angles into shared memory, one angle per
+// thread: the upper 32 bits of position * turns are the phase in turns to
+// 2^-32, a signed fraction in [-1/2, 1/2)
+__device__ __forceinline__ void fill_angles(const RopeFreq& f, const int32_t* positions, int n0, int ntok, float* cs,
+                                            int* status) {
+  for (int i = threadIdx.x; i < ntok * kHalf; i += kThreads) {
+    int pos = positions[n0 + i / kHalf];
+    if (pos < 0) {
+      if (i % kHalf == 0) atomicOr(status, kStatusData);
+      pos = 0;
+    }
+    const unsigned long long ph = (unsigned long long)(unsigned)pos * f.turns[i % kHalf];
+    const float turn = (float)(int)(unsigned)(ph >> 32) * 2.3283064365386963e-10f;  // 2^-32
+    float s, c;
+    sincospif(2.0f * turn, &s, &c);
+    cs[(i / kHalf) * 2 * kHalf + i % kHalf] = c;
+    cs[(i / kHalf) * 2 * kHalf + kHalf + i % kHalf] = s;
+  }
+}
+
+template <typename T>
+struct FwdArgs {
+  const T *q, *k, *v;
+  T *qo, *ko, *vo;
+  long long ldq, ldk, ldv, ldqo, ldko, ldvo;  // row strides, elements
+  const int32_t *positions, *slots;
+  int N, H, Hkv, tok;  // tok: tokens per CTA
+  long long out_rows;
+  float alpha, eps;
+  int* status;
+  RopeFreq f;
+};
+
+// A CTA takes `tok` tokens; its 32 eight-lane groups share them out evenly,
+// and a group walks every (32 / tok)-th head vector of its token with the
+// token's angles in registers.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant__ FwdArgs<T> a) {
+  __shared__ float cs[8 * 2 * kHalf];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n0 = blockIdx.x * a.tok;
+  const int ntok = min(a.tok, a.N - n0);
+  fill_angles(a.f, a.positions, n0, ntok, cs, a.status);
+  __syncthreads();
+  const int group = threadIdx.x >> 3, j = threadIdx.x & 7;
+  const int per = 32 / a.tok;  // groups per token
+  const int tl = group / per;
+  if (tl >= ntok) return;
+  const unsigned mask = 0xffu << ((threadIdx.x & 31) & ~7);
+  const int n = n0 + tl;
+  long long slot = a.slots != nullptr ? (long long)a.slots[n] : (long long)n;
+  if (slot < -1 || slot >= a.out_rows) {  // -1: a token that is not kept
+    if (group % per == 0 && j == 0) atomicOr(a.status, kStatusData);
+    slot = -1;
+  }
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i] = cs[tl * 2 * kHalf + 8 * j + i];
+    s[i] = cs[tl * 2 * kHalf + kHalf + 8 * j + i];
+  }
+  const int heads = a.H + (slot >= 0 ? (a.v != nullptr ? 2 : 1) * a.Hkv : 0);
+#pragma unroll 2
+  for (int h = group % per; h < heads; h += per) {
+    const int hk = h - a.H, hv = hk - a.Hkv;
+    const T* src = hk < 0 ? a.q + n * a.ldq + h * kD : (hv < 0 ? a.k + n * a.ldk + hk * kD : a.v + n * a.ldv + hv * kD);
+    T* dst = hk < 0 ? a.qo + n * a.ldqo + h * kD
+                    : (hv < 0 ? a.ko + slot * a.ldko + hk * kD : a.vo + slot * a.ldvo + hv * kD);
+    Raw<T> raw;
+    raw.load(src, j);
+    if (hv < 0) {
+      Vec x = raw.get();
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += x.a[i] * x.a[i] + x.b[i] * x.b[i];
+      ss = sum8(ss, mask);
+      const float r = a.alpha * rsqrtf(ss * (1.0f / kD) + a.eps);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float u = x.a[i], w = x.b[i];
+        x.a[i] = r * (u * c[i] - w * s[i]);
+        x.b[i] = r * (w * c[i] + u * s[i]);
+      }
+      raw.set(x);
+    }
+    raw.store(dst, j);
+  }
+}
+
+template <typename T>
+struct BwdArgs {
+  const T *q, *k, *gq, *gk;
+  T *dq, *dk;
+  long long ldq, ldk, ldgq, ldgk, lddq, lddk;
+  const int32_t* positions;
+  int N, H, Hkv, tok;
+  float alpha, eps;
+  int* status;
+  RopeFreq f;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_qk_norm_rope_bwd(const __grid_constant__ BwdArgs<T> a) {
+  __shared__ float cs[8 * 2 * kHalf];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n0 = blockIdx.x * a.tok;
+  const int ntok = min(a.tok, a.N - n0);
+  fill_angles(a.f, a.positions, n0, ntok, cs, a.status);
+  __syncthreads();
+  const int group = threadIdx.x >> 3, j = threadIdx.x & 7;
+  const int per = 32 / a.tok;
+  const int tl = group / per;
+  if (tl >= ntok) return;
+  const unsigned mask = 0xffu << ((threadIdx.x & 31) & ~7);
+  const int n = n0 + tl;
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i] = cs[tl * 2 * kHalf + 8 * j + i];
+    s[i] = cs[tl * 2 * kHalf + kHalf + 8 * j + i];
+  }
+#pragma unroll 2
+  for (int h = group % per; h < a.H + a.Hkv; h += per) {
+    const int hk = h - a.H;
+    Raw<T> rx, rg;
+    rx.load(hk < 0 ? a.q + n * a.ldq + h * kD : a.k + n * a.ldk + hk * kD, j);
+    rg.load(hk < 0 ? a.gq + n * a.ldgq + h * kD : a.gk + n * a.ldgk + hk * kD, j);
+    const Vec x = rx.get();
+    Vec g = rg.get();
+    float ss = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float u = g.a[i], w = g.b[i];
+      g.a[i] = u * c[i] + w * s[i];
+      g.b[i] = w * c[i] - u * s[i];
+      ss += x.a[i] * x.a[i] + x.b[i] * x.b[i];
+      dot += x.a[i] * g.a[i] + x.b[i] * g.b[i];
+    }
+    ss = sum8(ss, mask);
+    dot = sum8(dot, mask);
+    const float inv = rsqrtf(ss * (1.0f / kD) + a.eps);
+    const float r = a.alpha * inv, t = dot * (1.0f / kD) * inv * inv;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      g.a[i] = r * (g.a[i] - x.a[i] * t);
+      g.b[i] = r * (g.b[i] - x.b[i] * t);
+    }
+    rg.set(g);
+    rg.store(hk < 0 ? a.dq + n * a.lddq + h * kD : a.dk + n * a.lddk + hk * kD, j);
+  }
+}
+
+// base^(-2i/D) / (2 pi) as fractions of 2^64, by repeated multiplication in
+// long double (64 factors: relative error below 2^-57)
+void rope_freq(float base, RopeFreq* f) {
+  const long double ratio = expl(-logl((long double)base) / kHalf);
+  long double t = 0.15915494309189533576888376337251436203L;  // 1 / (2 pi)
+  for (int i = 0; i < kHalf; ++i, t *= ratio) f->turns[i] = (unsigned long long)(t * 18446744073709551616.0L);
+}
+
+int tokens_per_cta(int N) { return N >= 4 * 1024 ? 4 : 1; }
+
+}  // namespace
+
+template <typename T>
+static void run_fwd(const QkNormArgs& p, cudaStream_t st) {
+  FwdArgs<T> a;
+  a.q = static_cast<const T*>(p.q), a.k = static_cast<const T*>(p.k), a.v = static_cast<const T*>(p.v);
+  a.qo = static_cast<T*>(p.q_out), a.ko = static_cast<T*>(p.k_out), a.vo = static_cast<T*>(p.v_out);
+  a.ldq = p.ldq, a.ldk = p.ldk, a.ldv = p.ldv, a.ldqo = p.ldqo, a.ldko = p.ldko, a.ldvo = p.ldvo;
+  a.positions = p.positions, a.slots = p.slots;
+  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.tok = tokens_per_cta(p.N);
+  a.out_rows = p.out_rows, a.alpha = p.alpha, a.eps = p.eps, a.status = p.status;
+  rope_freq(p.rope_base, &a.f);
+  LaunchScope scope_(KK_QK_NORM_ROPE, st);
+  launch_pdl(k_qk_norm_rope<T>, dim3((p.N + a.tok - 1) / a.tok), dim3(kThreads), 0, st, 1, a);
+}
+
+void launch_qk_norm_rope(const QkNormArgs& p, int act_bf16, cudaStream_t st) {
+  if (act_bf16)
+    run_fwd<bf16>(p, st);
+  else
+    run_fwd<float>(p, st);
+}
+
+template <typename T>
+static void run_bwd(const QkNormArgs& p, cudaStream_t st) {
+  BwdArgs<T> a;
+  a.q = static_cast<const T*>(p.q), a.k = static_cast<const T*>(p.k);
+  a.gq = static_cast<const T*>(p.dq_hat), a.gk = static_cast<const T*>(p.dk_hat);
+  a.dq = static_cast<T*>(p.q_out), a.dk = static_cast<T*>(p.k_out);
+  a.ldq = p.ldq, a.ldk = p.ldk, a.ldgq = p.ldgq, a.ldgk = p.ldgk, a.lddq = p.ldqo, a.lddk = p.ldko;
+  a.positions = p.positions;
+  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.tok = tokens_per_cta(p.N);
+  a.alpha = p.alpha, a.eps = p.eps, a.status = p.status;
+  rope_freq(p.rope_base, &a.f);
+  LaunchScope scope_(KK_QK_NORM_ROPE, st);
+  launch_pdl(k_qk_norm_rope_bwd<T>, dim3((p.N + a.tok - 1) / a.tok), dim3(kThreads), 0, st, 1, a);
+}
+
+void launch_qk_norm_rope_bwd(const QkNormArgs& p, int act_bf16, cudaStream_t st) {
+  if (act_bf16)
+    run_bwd<bf16>(p, st);
+  else
+    run_bwd<float>(p, st);
+}
+
+}  // namespace nc

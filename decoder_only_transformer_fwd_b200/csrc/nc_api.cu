@@ -854,6 +854,182 @@ int nc_prefix_ce(const float* x, const void* w_u, const int32_t* targets, float*
   return check_launch("nc_prefix_ce");
 }
 
+static bool row_stride_ok(long long ld, int act_bf16) { return ld % (act_bf16 ? 8 : 4) == 0; }
+
+// arrays of int32 or fp32 read one element at a time
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks that the two directions of QK-norm share; NC_OK or the error.
+static int qk_norm_check(const QkNormArgs& p, int D, int dtype) {
+  if (!(p.alpha > 0.f) || !std::isfinite(p.alpha) || !(p.rope_base >= 1.f) || !std::isfinite(p.rope_base) ||
+      !(p.eps >= 0.f) || !std::isfinite(p.eps))
+    return NC_ERR_ARG;
+  if (dtype != NC_BF16 && dtype != NC_FP32) return NC_ERR_ARG;
+  if (p.N < 0 || p.H <= 0 || p.Hkv <= 0 || D != 128 || p.H % p.Hkv != 0 || p.H > (1 << 20)) return NC_ERR_SHAPE;
+  return NC_OK;
+}
+
+int nc_qk_norm_rope(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
+                    const int32_t* positions, const int32_t* slots, int N, int H, int Hkv, int D, void* q_out,
+                    long long ldqo, void* k_out, long long ldko, void* v_out, long long ldvo, long long out_rows,
+                    float alpha, float rope_base, float eps, int dtype, void* stream) {
+  t_launches = 0;
+  QkNormArgs p;
+  memset(&p, 0, sizeof(p));
+  p.q = q, p.k = k, p.v = v, p.q_out = q_out, p.k_out = k_out, p.v_out = v_out;
+  p.ldq = ldq, p.ldk = ldk, p.ldv = ldv, p.ldqo = ldqo, p.ldko = ldko, p.ldvo = ldvo;
+  p.positions = positions, p.slots = slots, p.N = N, p.H = H, p.Hkv = Hkv, p.out_rows = out_rows;
+  p.alpha = alpha, p.rope_base = rope_base, p.eps = eps;
+  if (!q || !k || !positions || !q_out || !k_out || (v == nullptr) != (v_out == nullptr)) return NC_ERR_ARG;
+  const int rc = qk_norm_check(p, D, dtype);
+  if (rc != NC_OK) return rc;
+  if (out_rows < 0 || (slots == nullptr && out_rows < N)) return NC_ERR_SHAPE;
+  if (ldq < (long long)H * D || ldqo < (long long)H * D || ldk < (long long)Hkv * D || ldko < (long long)Hkv * D ||
+      (v && (ldv < (long long)Hkv * D || ldvo < (long long)Hkv * D)))
+    return NC_ERR_SHAPE;
+  const int bf = dtype == NC_BF16;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(v_out) ||
+      !aligned4(positions) || !aligned4(slots) || !row_stride_ok(ldq, bf) || !row_stride_ok(ldk, bf) || !row_stride_ok(ldqo, bf) ||
+      !row_stride_ok(ldko, bf) || (v && (!row_stride_ok(ldv, bf) || !row_stride_ok(ldvo, bf))))
+    return NC_ERR_ALIGN;
+  if (N == 0) return NC_OK;
+  DevInfo d;
+  if (!dev_info(&d)) return NC_ERR_CUDA;
+  p.status = d.status;
+  launch_qk_norm_rope(p, bf, static_cast<cudaStream_t>(stream));
+  return check_launch("nc_qk_norm_rope");
+}
+
+int nc_qk_norm_rope_backward(const void* q, long long ldq, const void* k, long long ldk, const int32_t* positions,
+                             const void* dq_hat, long long ldgq, const void* dk_hat, long long ldgk, int N, int H,
+                             int Hkv, int D, void* out_dq, long long lddq, void* out_dk, long long lddk, float alpha,
+                             float rope_base, float eps, int dtype, void* stream) {
+  t_launches = 0;
+  QkNormArgs p;
+  memset(&p, 0, sizeof(p));
+  p.q = q, p.k = k, p.dq_hat = dq_hat, p.dk_hat = dk_hat, p.q_out = out_dq, p.k_out = out_dk;
+  p.ldq = ldq, p.ldk = ldk, p.ldgq = ldgq, p.ldgk = ldgk, p.ldqo = lddq, p.ldko = lddk;
+  p.positions = positions, p.N = N, p.H = H, p.Hkv = Hkv;
+  p.alpha = alpha, p.rope_base = rope_base, p.eps = eps;
+  if (!q || !k || !positions || !dq_hat || !dk_hat || !out_dq || !out_dk) return NC_ERR_ARG;
+  const int rc = qk_norm_check(p, D, dtype);
+  if (rc != NC_OK) return rc;
+  if (ldq < (long long)H * D || ldgq < (long long)H * D || lddq < (long long)H * D || ldk < (long long)Hkv * D ||
+      ldgk < (long long)Hkv * D || lddk < (long long)Hkv * D)
+    return NC_ERR_SHAPE;
+  const int bf = dtype == NC_BF16;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(dq_hat) || !aligned16(dk_hat) || !aligned16(out_dq) ||
+      !aligned16(out_dk) || !aligned4(positions) || !row_stride_ok(ldq, bf) || !row_stride_ok(ldk, bf) || !row_stride_ok(ldgq, bf) ||
+      !row_stride_ok(ldgk, bf) || !row_stride_ok(lddq, bf) || !row_stride_ok(lddk, bf))
+    return NC_ERR_ALIGN;
+  if (N == 0) return NC_OK;
+  DevInfo d;
+  if (!dev_info(&d)) return NC_ERR_CUDA;
+  p.status = d.status;
+  launch_qk_norm_rope_bwd(p, bf, static_cast<cudaStream_t>(stream));
+  return check_launch("nc_qk_norm_rope_backward");
+}
+
+// Sizes of a shared-prefix attention call and how its work is cut; false on
+// sizes the kernel does not take.
+static bool prefix_attn_sizes(PrefixAttnArgs* a, int B, int G, int Tq, int H, int Hkv, int P_max, int S_max, int window) {
+  memset(a, 0, sizeof(*a));
+  if (B <= 0 || G <= 0 || B % G != 0 || Tq <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || H / Hkv > 128) return false;
+  if (P_max < 0 || S_max < 0 || (long long)P_max + S_max == 0 || (long long)P_max + S_max > (1 << 30)) return false;
+  if ((long long)B * Tq > 0x7fffffffLL / H) return false;
+  a->B = B, a->G = G, a->Tq = Tq, a->H = H, a->Hkv = Hkv, a->P_max = P_max, a->S_max = S_max;
+  a->window = (window <= 0 || window > P_max + S_max) ? P_max + S_max : window;
+  return prefix_attn_plan(a);
+}
+
+static size_t prefix_attn_bytes(const PrefixAttnArgs& a, size_t* lse_at) {
+  const size_t parts = (size_t)a.splits_p + a.splits_s, rows = (size_t)a.B * a.Tq * a.H;
+  *lse_at = parts * rows * 512;
+  return parts == 1 ? 0 : *lse_at + align256(parts * rows * 4);
+}
+
+size_t nc_prefix_attention_workspace_bytes(int B, int G, int Tq, int H, int Hkv, int P_max, int S_max, int window) {
+  PrefixAttnArgs a;
+  size_t at;
+  return prefix_attn_sizes(&a, B, G, Tq, H, Hkv, P_max, S_max, window) ? prefix_attn_bytes(a, &at) : 0;
+}
+
+int nc_prefix_attention(const void* q, long long ldq, const void* k_prefix, const void* v_prefix, long long ldp,
+                        long long lsp, const int32_t* prefix_lens, const void* k_suffix, const void* v_suffix,
+                        long long lds, long long lss, const int32_t* suffix_lens, void* out, float* out_lse_opt, int B,
+                        int G, int Tq, int H, int Hkv, int D, int P_max, int S_max, int window, float softmax_scale,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  t_launches = 0;
+  if (!q || !out || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return NC_ERR_ARG;
+  if (P_max > 0 && (!k_prefix || !v_prefix || !prefix_lens)) return NC_ERR_ARG;
+  if (S_max > 0 && (!k_suffix || !v_suffix || !suffix_lens)) return NC_ERR_ARG;
+  PrefixAttnArgs a;
+  if (D != 128 || !prefix_attn_sizes(&a, B, G, Tq, H, Hkv, P_max, S_max, window)) return NC_ERR_SHAPE;
+  const long long kv = (long long)Hkv * D, far = 1LL << 38;  // strides in bytes stay below 2^40
+  if (ldq < (long long)H * D || ldq > far / ((long long)B * Tq)) return NC_ERR_SHAPE;
+  if (P_max > 0 && (ldp < kv || ldp > far / P_max || (G > 1 && (lsp < ldp * (P_max - 1) + kv || lsp > far)))) return NC_ERR_SHAPE;
+  if (S_max > 0 && (lds < kv || lds > far / S_max || (B > 1 && (lss < lds * (S_max - 1) + kv || lss > far)))) return NC_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(out_lse_opt) || !aligned16(workspace) || ldq % 8 != 0 ||
+      !aligned4(prefix_lens) || !aligned4(suffix_lens))
+    return NC_ERR_ALIGN;
+  if (P_max > 0 && (!aligned16(k_prefix) || !aligned16(v_prefix) || ldp % 8 != 0 || (G > 1 && lsp % 8 != 0))) return NC_ERR_ALIGN;
+  if (S_max > 0 && (!aligned16(k_suffix) || !aligned16(v_suffix) || lds % 8 != 0 || (B > 1 && lss % 8 != 0))) return NC_ERR_ALIGN;
+  size_t lse_at;
+  const size_t need = prefix_attn_bytes(a, &lse_at);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return NC_ERR_WORKSPACE;
+  DevInfo d;
+  if (!dev_info(&d)) return NC_ERR_CUDA;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.prefix_lens = P_max > 0 ? prefix_lens : nullptr;
+  a.suffix_lens = S_max > 0 ? suffix_lens : nullptr;
+  a.out = static_cast<bf16*>(out);
+  a.out_lse = out_lse_opt;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = need > 0 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + lse_at) : nullptr;
+  a.status = d.status;
+  if (!launch_prefix_attn(a, q, ldq, k_prefix, v_prefix, ldp, lsp, k_suffix, v_suffix, lds, lss,
+                          static_cast<cudaStream_t>(stream))) {
+    check_launch("nc_prefix_attention");
+    return NC_ERR_CUDA;
+  }
+  return check_launch("nc_prefix_attention");
+}
+
+size_t nc_policy_loss_workspace_bytes(void) { return (size_t)kPolicyMaxCtas * 3 * sizeof(double); }
+
+int nc_policy_loss(const void* logits, long long ldl, const int32_t* targets, const float* advantages, int adv_per_token,
+                   const float* old_logp_opt, const float* ref_logp_opt, int B, int T, int V, float clip_low,
+                   float clip_high, float kl_beta, int norm, float* out_stats, float* out_logp, void* out_dlogits_opt,
+                   long long lddl, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  t_launches = 0;
+  if (!logits || !targets || !advantages || !out_stats || !out_logp) return NC_ERR_ARG;
+  if (!(clip_low >= 0.f) || !(clip_low < 1.f) || !(clip_high >= 0.f) || !std::isfinite(clip_high) ||
+      !(kl_beta >= 0.f) || !std::isfinite(kl_beta) || (norm != 0 && norm != 1) ||
+      (adv_per_token != 0 && adv_per_token != 1) || (dtype != NC_BF16 && dtype != NC_FP32))
+    return NC_ERR_ARG;
+  if (B <= 0 || T <= 0 || V <= 0 || (long long)B * T > 0x7fffffffLL || V > (1 << 30) || ldl < V ||
+      (out_dlogits_opt && lddl < V))
+    return NC_ERR_SHAPE;
+  const uintptr_t esz = dtype == NC_BF16 ? 2 : 4;  // rows may start anywhere, elements may not
+  if (reinterpret_cast<uintptr_t>(logits) % esz || reinterpret_cast<uintptr_t>(out_dlogits_opt) % esz ||
+      !aligned4(targets) || !aligned4(advantages) || !aligned4(old_logp_opt) || !aligned4(ref_logp_opt) ||
+      !aligned4(out_stats) || !aligned4(out_logp) || !aligned16(workspace))
+    return NC_ERR_ALIGN;
+  if (workspace == nullptr || workspace_bytes < nc_policy_loss_workspace_bytes()) return NC_ERR_WORKSPACE;
+  DevInfo d;
+  if (!dev_info(&d)) return NC_ERR_CUDA;
+  PolicyArgs a;
+  memset(&a, 0, sizeof(a));
+  a.logits = logits, a.ldl = ldl, a.targets = targets, a.advantages = advantages, a.adv_per_token = adv_per_token;
+  a.old_logp = old_logp_opt, a.ref_logp = ref_logp_opt, a.B = B, a.T = T, a.V = V, a.norm = norm;
+  a.ratio_low = 1.0 - (double)clip_low, a.ratio_high = 1.0 + (double)clip_high;
+  a.log_low = log(a.ratio_low), a.log_high = log(a.ratio_high);
+  a.kl_beta = kl_beta, a.out_stats = out_stats, a.out_logp = out_logp, a.dlogits = out_dlogits_opt, a.lddl = lddl;
+  a.status = d.status;
+  launch_policy_loss(a, dtype == NC_BF16, static_cast<double*>(workspace), d.num_sms, static_cast<cudaStream_t>(stream));
+  return check_launch("nc_policy_loss");
+}
+
 int nc_get_status(void* stream, int* out_bits) {
   DevInfo d;
   if (!dev_info(&d)) return NC_ERR_CUDA;
@@ -914,7 +1090,8 @@ const char* nc_kernel_name(int kind) {
   static const char* names[KK_COUNT] = {
       "embed_norm_smear", "rmsnorm", "rope_table", "rope_qknorm", "gemm_tcgen05", "gemm_cuda_core",
       "attention_tcgen05", "attention_cuda_core", "ce_combine", "ce_rows", "loss_mean", "last_logits",
-      "sample", "gemm_tcgen05_bwd", "head_bwd_rows", "prefix_rmsnorm"};
+      "sample", "gemm_tcgen05_bwd", "head_bwd_rows", "prefix_rmsnorm", "qk_norm_rope", "prefix_attention",
+      "policy_loss"};
   return (kind >= 0 && kind < KK_COUNT) ? names[kind] : "unknown";
 }
 

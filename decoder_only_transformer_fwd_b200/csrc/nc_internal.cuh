@@ -210,6 +210,57 @@ bool launch_attn_tc(const bf16* q, const bf16* k, const bf16* v, int ldq, int ld
                     int ldo, int B, int T, int H, int Hkv, int window, float scale, int* status,
                     int num_sms, cudaStream_t st);
 
+// QK-norm with RoPE at given positions (k_qknorm.cu); strides in elements.
+// The backward takes dq_hat / dk_hat and writes dx through q_out / k_out.
+struct QkNormArgs {
+  const void *q, *k, *v, *dq_hat, *dk_hat;
+  void *q_out, *k_out, *v_out;
+  long long ldq, ldk, ldv, ldgq, ldgk, ldqo, ldko, ldvo;
+  const int32_t *positions, *slots;
+  int N, H, Hkv;
+  long long out_rows;
+  float alpha, rope_base, eps;
+  int* status;
+};
+void launch_qk_norm_rope(const QkNormArgs& p, int act_bf16, cudaStream_t st);
+void launch_qk_norm_rope_bwd(const QkNormArgs& p, int act_bf16, cudaStream_t st);
+
+// Attention over a shared prefix and the rows' own keys (k_prefix_attn.cu).
+constexpr int kPrefixMaxSplits = 128;
+struct PrefixAttnArgs {
+  int B, G, Tq, H, Hkv, P_max, S_max, window;
+  float scale_log2;  // softmax_scale * log2(e)
+  const int32_t *prefix_lens, *suffix_lens;
+  bf16* out;
+  float* out_lse;
+  float *part_o, *part_lse;  // workspace: [parts, B Tq H, 128] and [parts, B Tq H]
+  int* status;
+  // filled by prefix_attn_plan()
+  int rows_per_group, box_p, box_s, tiles_p, tiles_s, splits_p, splits_s, min_tiles, units_p, units;
+};
+// false where the units do not fit an int
+bool prefix_attn_plan(PrefixAttnArgs* a);
+bool launch_prefix_attn(const PrefixAttnArgs& a, const void* q, long long ldq, const void* kp, const void* vp,
+                        long long ldp, long long lsp, const void* ks, const void* vs, long long lds, long long lss,
+                        cudaStream_t st);
+
+// Clipped policy loss (k_policy.cu); part: 3 doubles per CTA.
+constexpr int kPolicyMaxCtas = 1024;
+struct PolicyArgs {
+  const void* logits;
+  long long ldl;
+  const int32_t* targets;
+  const float *advantages, *old_logp, *ref_logp;
+  int adv_per_token, B, T, V, norm;
+  double log_low, log_high, ratio_low, ratio_high;
+  float kl_beta;
+  float *out_stats, *out_logp;
+  void* dlogits;
+  long long lddl;
+  int* status;
+};
+void launch_policy_loss(const PolicyArgs& a, int act_bf16, double* part, int num_sms, cudaStream_t st);
+
 // Raise `kernel`'s dynamic shared-memory limit to `bytes` on the current
 // device.  The attribute belongs to the device's context, so it is set per
 // (kernel, device): a process that drives several devices sets it on each,
@@ -236,7 +287,7 @@ int check_launch(const char* what);
 enum KernelKind : int {
   KK_EMBED = 0, KK_RMSNORM, KK_ROPE_TABLE, KK_ROPE_QKNORM, KK_GEMM_TC, KK_GEMM_SIMT, KK_ATTN_TC,
   KK_ATTN_SIMT, KK_CE_COMBINE, KK_CE_ROWS, KK_LOSS_MEAN, KK_LAST_LOGITS, KK_SAMPLE, KK_GEMM_TC_BWD,
-  KK_HEAD_BWD_ROWS, KK_PREFIX_NORM, KK_COUNT
+  KK_HEAD_BWD_ROWS, KK_PREFIX_NORM, KK_QK_NORM_ROPE, KK_PREFIX_ATTN, KK_POLICY_LOSS, KK_COUNT
 };
 // Every launcher holds one of these around its kernel launch: it counts the
 // launch (per host thread) and, when the caller enabled timing for this kind,

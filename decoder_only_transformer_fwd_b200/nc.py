@@ -95,11 +95,25 @@ _SIGS = {
     "nc_head_backward_workspace_bytes": (C.c_size_t, [C.POINTER(nc_config), C.c_int]),
     "nc_head_backward": (C.c_int, [C.POINTER(nc_params), C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
                                    C.c_void_p, C.c_size_t, C.c_void_p]),
+    "nc_qk_norm_rope": (C.c_int, [C.c_void_p, C.c_longlong] * 3 + [C.c_void_p] * 2 + [C.c_int] * 4
+                        + [C.c_void_p, C.c_longlong] * 3 + [C.c_longlong] + [C.c_float] * 3 + [C.c_int, C.c_void_p]),
+    "nc_qk_norm_rope_backward": (C.c_int, [C.c_void_p, C.c_longlong] * 2 + [C.c_void_p] + [C.c_void_p, C.c_longlong] * 2
+                                 + [C.c_int] * 4 + [C.c_void_p, C.c_longlong] * 2 + [C.c_float] * 3
+                                 + [C.c_int, C.c_void_p]),
+    "nc_prefix_attention_workspace_bytes": (C.c_size_t, [C.c_int] * 8),
+    "nc_prefix_attention": (C.c_int, [C.c_void_p, C.c_longlong]
+                            + ([C.c_void_p] * 2 + [C.c_longlong] * 2 + [C.c_void_p]) * 2 + [C.c_void_p] * 2
+                            + [C.c_int] * 9 + [C.c_float, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "nc_policy_loss_workspace_bytes": (C.c_size_t, []),
+    "nc_policy_loss": (C.c_int, [C.c_void_p, C.c_longlong, C.c_void_p, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p]
+                       + [C.c_int] * 3 + [C.c_float] * 3 + [C.c_int] + [C.c_void_p] * 3
+                       + [C.c_longlong, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p]),
 }
 
 KERNEL_KINDS = ["embed_norm_smear", "rmsnorm", "rope_table", "rope_qknorm", "gemm_tcgen05",
                 "gemm_cuda_core", "attention_tcgen05", "attention_cuda_core", "ce_combine", "ce_rows",
-                "loss_mean", "last_logits", "sample", "gemm_tcgen05_bwd", "head_bwd_rows", "prefix_rmsnorm"]
+                "loss_mean", "last_logits", "sample", "gemm_tcgen05_bwd", "head_bwd_rows", "prefix_rmsnorm",
+                "qk_norm_rope", "prefix_attention", "policy_loss"]
 
 
 class LaunchTimer:
@@ -324,6 +338,209 @@ def nc_prefix_ce(x, w_u, targets, out_loss, vocab: int, widths, eps: float = 1e-
     nbytes = workspace.numel() * workspace.element_size()
     _check(lib().nc_prefix_ce(_ptr(x), _ptr(w_u), _ptr(targets), _ptr(out_loss), M, Cw, vocab, V_pad, wd, k, eps,
                               cap, _ptr(workspace), nbytes, _stream(stream)), "nc_prefix_ce")
+
+
+def _operands(what: str, *items):
+    """Checks tensors before their pointers are handed over.  items: (name,
+    tensor or None, shape with None for any size, dtype).  All tensors must be
+    on the current CUDA device: the call runs there, on one of its streams."""
+    import torch
+    dev = None
+    for name, t, shape, dtype in items:
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise NcError(f"{what}: {name} is {t.dtype}, expected {dtype}")
+        if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+            raise NcError(f"{what}: {name} has shape {tuple(t.shape)}, expected {shape}")
+        if not t.is_cuda:
+            raise NcError(f"{what}: {name} is not on a CUDA device")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise NcError(f"{what}: {name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _packed(what: str, name: str, t, first: int = 0):
+    """t's dimensions from `first` on are laid out without gaps."""
+    if t is None or t.is_contiguous() and first == 0:
+        return
+    want = 1
+    for n, s in zip(reversed(t.shape[first:]), reversed(t.stride()[first:])):
+        if n > 1 and s != want:
+            raise NcError(f"{what}: {name} has strides {tuple(t.stride())}: "
+                          f"its last {t.dim() - first} dimension(s) must be contiguous")
+        want *= n
+
+
+def _act_dtype(what: str, t):
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise NcError(f"{what}: {t.dtype} is not supported (bfloat16 or float32)")
+    return NC_BF16 if t.dtype == torch.bfloat16 else NC_FP32
+
+
+def _row(t):
+    """Row stride of t [rows, ...]; a single row has any."""
+    return 0 if t is None else (t.stride(0) if t.shape[0] > 1 else t[0].numel())
+
+
+def _scratch(workspace, nbytes: int, like):
+    """(workspace, its bytes): the caller's, or a new one of nbytes."""
+    import torch
+    if workspace is None and nbytes > 0:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if workspace is None:
+        return None, 0
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise NcError("workspace: a contiguous tensor on the operands' device is needed")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def nc_qk_norm_rope(q, k, positions, q_out, k_out, v=None, v_out=None, slots=None, alpha: float = 1.15,
+                    rope_base: float = 100000.0, eps: float = 1e-6, stream=None):
+    """qhat [N, H, D] and khat of tokens q [N, H, D], k [N, H_kv, D] at positions [N] (int32); khat and v
+    go to rows slots [N] (int32, -1 = not kept) of k_out and v_out [rows, H_kv, D], or to rows 0..N-1."""
+    import torch
+    what = "nc_qk_norm_rope"
+    dt = _act_dtype(what, q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise NcError(f"{what}: q and k are [N, heads, D]")
+    N, H, D = q.shape
+    Hkv, rows = k.shape[1], k_out.shape[0]
+    if (v is None) != (v_out is None):
+        raise NcError(f"{what}: v and v_out come together")
+    _operands(what, ("q", q, (N, H, D), q.dtype), ("k", k, (N, Hkv, D), q.dtype), ("v", v, (N, Hkv, D), q.dtype),
+              ("positions", positions, (N,), torch.int32), ("slots", slots, (N,), torch.int32),
+              ("q_out", q_out, (N, H, D), q.dtype), ("k_out", k_out, (rows, Hkv, D), q.dtype),
+              ("v_out", v_out, (rows, Hkv, D), q.dtype))
+    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out), ("v_out", v_out)):
+        _packed(what, name, t, 1)
+    _packed(what, "positions", positions)
+    _packed(what, "slots", slots)
+    if N == 0:
+        return
+    _check(lib().nc_qk_norm_rope(_ptr(q), _row(q), _ptr(k), _row(k), _ptr(v), _row(v), _ptr(positions), _ptr(slots),
+                                 N, H, Hkv, D, _ptr(q_out), _row(q_out), _ptr(k_out), _row(k_out) if rows else Hkv * D,
+                                 _ptr(v_out), (_row(v_out) if rows else Hkv * D) if v_out is not None else 0, rows,
+                                 alpha, rope_base, eps, dt, _stream(stream)), what)
+
+
+def nc_qk_norm_rope_backward(q, k, positions, dq_hat, dk_hat, out_dq, out_dk, alpha: float = 1.15,
+                             rope_base: float = 100000.0, eps: float = 1e-6, stream=None):
+    """Gradients of q [N, H, D] and k [N, H_kv, D] from those of nc_qk_norm_rope's qhat and khat."""
+    import torch
+    what = "nc_qk_norm_rope_backward"
+    dt = _act_dtype(what, q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise NcError(f"{what}: q and k are [N, heads, D]")
+    N, H, D = q.shape
+    Hkv = k.shape[1]
+    _operands(what, ("q", q, (N, H, D), q.dtype), ("k", k, (N, Hkv, D), q.dtype),
+              ("positions", positions, (N,), torch.int32), ("dq_hat", dq_hat, (N, H, D), q.dtype),
+              ("dk_hat", dk_hat, (N, Hkv, D), q.dtype), ("out_dq", out_dq, (N, H, D), q.dtype),
+              ("out_dk", out_dk, (N, Hkv, D), q.dtype))
+    for name, t in (("q", q), ("k", k), ("dq_hat", dq_hat), ("dk_hat", dk_hat), ("out_dq", out_dq), ("out_dk", out_dk)):
+        _packed(what, name, t, 1)
+    _packed(what, "positions", positions)
+    if N == 0:
+        return
+    _check(lib().nc_qk_norm_rope_backward(_ptr(q), _row(q), _ptr(k), _row(k), _ptr(positions), _ptr(dq_hat), _row(dq_hat),
+                                          _ptr(dk_hat), _row(dk_hat), N, H, Hkv, D, _ptr(out_dq), _row(out_dq),
+                                          _ptr(out_dk), _row(out_dk), alpha, rope_base, eps, dt, _stream(stream)), what)
+
+
+def nc_prefix_attention_workspace_bytes(B, G, Tq, H, Hkv, P_max, S_max, window: int = 0) -> int:
+    return int(lib().nc_prefix_attention_workspace_bytes(B, G, Tq, H, Hkv, P_max, S_max, window))
+
+
+def nc_prefix_attention(q, k_prefix, v_prefix, prefix_lens, k_suffix, v_suffix, suffix_lens, out, out_lse=None,
+                        window: int = 0, softmax_scale: float | None = None, workspace=None, stream=None):
+    """Attention of q [B, Tq, H, D] over the prefixes k_prefix, v_prefix [G, P_max, H_kv, D] that consecutive
+    rows share (prefix_lens [G] int32) and the rows' own k_suffix, v_suffix [B, S_max, H_kv, D]
+    (suffix_lens [B] int32); one side may be None.  out [B, Tq, H, D], out_lse [B, Tq, H] fp32."""
+    import torch
+    what = "nc_prefix_attention"
+    bf, i32 = torch.bfloat16, torch.int32
+    if q.dim() != 4:
+        raise NcError(f"{what}: q is [B, Tq, H, D]")
+    B, Tq, H, D = q.shape
+    sides = []
+    for side, k, v, lens, n in (("prefix", k_prefix, v_prefix, prefix_lens, None), ("suffix", k_suffix, v_suffix, suffix_lens, B)):
+        if (k is None) != (v is None) or (k is None) != (lens is None):
+            raise NcError(f"{what}: k, v and lengths of the {side} come together")
+        if k is None:
+            sides.append((None, None, 0, 0, None, 1, 0))
+            continue
+        if k.dim() != 4:
+            raise NcError(f"{what}: k_{side} is [sequences, keys, H_kv, D]")
+        seqs, cap, Hkv = k.shape[0], k.shape[1], k.shape[2]
+        _operands(what, (f"k_{side}", k, (n, None, None, D), bf), (f"v_{side}", v, tuple(k.shape), bf),
+                  (f"{side}_lens", lens, (seqs,), i32))
+        _packed(what, f"k_{side}", k, 2)
+        _packed(what, f"v_{side}", v, 2)
+        _packed(what, f"{side}_lens", lens)
+        ld = k.stride(1) if cap > 1 else Hkv * D
+        ls = k.stride(0) if seqs > 1 else ld * max(cap, 1)
+        if (cap > 1 and v.stride(1) != ld) or (seqs > 1 and v.stride(0) != ls):
+            raise NcError(f"{what}: k_{side} and v_{side} must have the same strides")
+        if cap == 0:
+            sides.append((None, None, 0, 0, None, seqs, 0))
+        else:
+            sides.append((k, v, ld, ls, lens, seqs, cap))
+    (kp, vp, ldp, lsp, pl, G, P), (ks, vs, lds, lss, sl, _, S) = sides
+    heads = {t.shape[2] for t in (k_prefix, k_suffix) if t is not None}
+    if len(heads) != 1:
+        raise NcError(f"{what}: " + ("there are no keys" if not heads else "prefix and suffix differ in key heads"))
+    Hkv = heads.pop()
+    _operands(what, ("q", q, (B, Tq, H, D), bf), ("out", out, (B, Tq, H, D), bf), ("out_lse", out_lse, (B, Tq, H), torch.float32))
+    _packed(what, "out", out)
+    _packed(what, "out_lse", out_lse)
+    _packed(what, "q", q, 2)
+    ldq = q.stride(1) if Tq > 1 else (q.stride(0) if B > 1 else H * D)
+    if B > 1 and Tq > 1 and q.stride(0) != Tq * ldq:
+        raise NcError(f"{what}: q's tokens must be evenly spaced (strides {tuple(q.stride())})")
+    scale = D ** -0.5 if softmax_scale is None else softmax_scale
+    workspace, nbytes = _scratch(workspace, nc_prefix_attention_workspace_bytes(B, G, Tq, H, Hkv, P, S, window), q)
+    _check(lib().nc_prefix_attention(_ptr(q), ldq, _ptr(kp), _ptr(vp), ldp, lsp, _ptr(pl), _ptr(ks), _ptr(vs), lds, lss,
+                                     _ptr(sl), _ptr(out), _ptr(out_lse), B, G, Tq, H, Hkv, D, P, S, window, scale,
+                                     _ptr(workspace), nbytes, _stream(stream)), what)
+
+
+def nc_policy_loss(logits, targets, advantages, out_stats, out_logp, out_dlogits=None, old_logp=None, ref_logp=None,
+                   clip_low: float = 0.2, clip_high: float = 0.2, kl_beta: float = 0.0, norm: int = 0, workspace=None,
+                   stream=None):
+    """Clipped policy loss of logits [B, T, V] (rows may be strided) at targets [B, T] (-1 = none) with advantages
+    [B] or [B, T]: out_stats [3] (loss, mean KL, clipped share), out_logp [B, T], out_dlogits [B, T, V]."""
+    import torch
+    what = "nc_policy_loss"
+    dt = _act_dtype(what, logits)
+    f32 = torch.float32
+    if logits.dim() != 3:
+        raise NcError(f"{what}: logits are [B, T, V]")
+    B, T, V = logits.shape
+    per_token = advantages.dim() == 2
+    _operands(what, ("logits", logits, (B, T, V), logits.dtype), ("targets", targets, (B, T), torch.int32),
+              ("advantages", advantages, (B, T) if per_token else (B,), f32), ("old_logp", old_logp, (B, T), f32),
+              ("ref_logp", ref_logp, (B, T), f32), ("out_stats", out_stats, (3,), f32), ("out_logp", out_logp, (B, T), f32),
+              ("out_dlogits", out_dlogits, (B, T, V), logits.dtype))
+    for name, t in (("targets", targets), ("advantages", advantages), ("old_logp", old_logp), ("ref_logp", ref_logp),
+                    ("out_stats", out_stats), ("out_logp", out_logp)):
+        _packed(what, name, t)
+
+    def row_stride(name, t):
+        _packed(what, name, t, 2)
+        ld = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else V)
+        if B > 1 and T > 1 and t.stride(0) != T * ld:
+            raise NcError(f"{what}: {name}'s rows must be evenly spaced (strides {tuple(t.stride())})")
+        return ld
+
+    ldl = row_stride("logits", logits)
+    lddl = row_stride("out_dlogits", out_dlogits) if out_dlogits is not None else 0
+    workspace, nbytes = _scratch(workspace, int(lib().nc_policy_loss_workspace_bytes()), logits)
+    _check(lib().nc_policy_loss(_ptr(logits), ldl, _ptr(targets), _ptr(advantages), int(per_token), _ptr(old_logp),
+                                _ptr(ref_logp), B, T, V, clip_low, clip_high, kl_beta, norm, _ptr(out_stats), _ptr(out_logp),
+                                _ptr(out_dlogits), lddl, dt, _ptr(workspace), nbytes, _stream(stream)), what)
 
 
 def nc_get_status(stream=None) -> tuple[int, int]:

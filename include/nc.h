@@ -45,7 +45,8 @@ typedef enum {
   NC_ERR_ALIGN = 3,      /* pointer or stride not 16-byte aligned            */
   NC_ERR_CUDA = 4,       /* a CUDA runtime call failed (see nc_last_error)   */
   NC_ERR_DATA = 5,       /* device-side: token/target id out of range, or a
-                            sampling uniform outside [0, 1)                   */
+                            sampling uniform outside [0, 1), or a length,
+                            position or cache slot out of range               */
   NC_ERR_TIMEOUT = 6,    /* device-side: a bounded wait inside a kernel ran out */
   NC_ERR_WORKSPACE = 7   /* workspace missing or smaller than required       */
 } nc_status;
@@ -332,6 +333,114 @@ int nc_prefix_ce(const float* x, const void* w_u, const int32_t* targets, float*
                  int V_pad, const int* widths, int k, float eps, float cap, void* workspace, size_t workspace_bytes,
                  void* stream);
 
+/* QK-norm with RoPE at given positions, written to dense rows or into a cache
+ * ([Math] §QK-Norm with Sharpening, §Rotary Position Embeddings): for every
+ * token n and head,
+ *   qhat = alpha R(positions[n]) q / sqrt(mean(q^2) + eps),
+ * likewise khat, with R the half-split rotation by position * rope_base^(-2i/D).
+ * One pass over q, k and v.  The tensors are rows of one token each, given by a
+ * pointer and a row stride in elements (so q, k and v may be slices of one
+ * projection's output):
+ *   q [N, H, D], k and v [N, H_kv, D], q_out [N, H, D], in `dtype`;
+ *   k_out and v_out [out_rows, H_kv, D]: khat and an unchanged copy of v of
+ *     token n go to row slots[n] (int32), or to row n when slots is NULL.
+ *     slots[n] == -1: the token's k and v are not kept (its qhat is written).
+ *     Rows that no token names are left as they were; tokens that name the same
+ *     row leave elements of any of them there.  v and v_out may both be NULL.
+ *   positions [N] int32, in [0, 2^31); angles are reduced exactly.
+ * An output may be its input (same pointer and stride; k and v only without
+ * slots); any other overlap is undefined.  A negative position is taken as 0
+ * and a slot outside [-1, out_rows) as -1; both set NC_ERR_DATA in the status
+ * word.  NC_ERR_SHAPE: D != 128, H % H_kv != 0, N < 0, a stride below its row's
+ * width, out_rows < N without slots.  NC_ERR_ALIGN: pointers not 16-byte
+ * aligned or strides not a multiple of 16 bytes.  NC_ERR_ARG: a missing
+ * pointer, alpha <= 0, rope_base < 1, eps < 0.  N == 0 does nothing. */
+int nc_qk_norm_rope(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
+                    const int32_t* positions, const int32_t* slots, int N, int H, int Hkv, int D, void* q_out,
+                    long long ldqo, void* k_out, long long ldko, void* v_out, long long ldvo, long long out_rows,
+                    float alpha, float rope_base, float eps, int dtype, void* stream);
+
+/* Gradient of nc_qk_norm_rope: from q, k (its inputs), positions and the
+ * gradients dq_hat [N, H, D], dk_hat [N, H_kv, D] of qhat and khat (row n =
+ * token n), out_dq [N, H, D] and out_dk [N, H_kv, D] in `dtype`:
+ *   dx = (alpha / rho) (b - x (x . b) / (D rho^2)),  b = R^T dxhat,
+ *   rho = sqrt(mean(x^2) + eps).
+ * v passes through unchanged, and so does its gradient.  out_dq may be q or
+ * dq_hat, out_dk may be k or dk_hat (same pointer and stride).  Checks and
+ * status codes as nc_qk_norm_rope. */
+int nc_qk_norm_rope_backward(const void* q, long long ldq, const void* k, long long ldk, const int32_t* positions,
+                             const void* dq_hat, long long ldgq, const void* dk_hat, long long ldgk, int N, int H,
+                             int Hkv, int D, void* out_dq, long long lddq, void* out_dk, long long lddk, float alpha,
+                             float rope_base, float eps, int dtype, void* stream);
+
+/* Attention of B rows in G groups of B / G consecutive rows, the rows of a group
+ * sharing a prefix (many samples of one prompt): row b sees the prefix_lens[g]
+ * keys of its group g = b / (B / G), positions 0 .. prefix_lens[g] - 1, then
+ * its own suffix_lens[b] keys.  Query i of the row's Tq has position
+ *   prefix_lens[g] + suffix_lens[b] - Tq + i
+ * (the last Tq tokens, their own keys already in the cache) and sees key j iff
+ * j <= position and position - j < window ([Math] §Scaled Dot-Product Attention
+ * with Sliding Window; window <= 0: no window):
+ *   o = sum_j softmax_j(softmax_scale * q . k_j) v_j.
+ * q and k as they enter the attention (nc_qk_norm_rope).  All bf16:
+ *   q [B, Tq, H, D], row stride ldq (elements between tokens);
+ *   k_prefix, v_prefix [G, P_max, H_kv, D]: ldp between keys, lsp between groups;
+ *   k_suffix, v_suffix [B, S_max, H_kv, D]: lds between keys, lss between rows;
+ *   out [B, Tq, H, D] contiguous; out_lse_opt [B, Tq, H] fp32 or NULL: the
+ *     log-sum-exp of the row's scaled scores.
+ * prefix_lens [G] and suffix_lens [B] are DEVICE int32, so a captured call
+ * follows them; lengths outside [0, P_max] or [0, S_max] are clamped and set
+ * NC_ERR_DATA.  Cache rows behind a length, or before every query's window, may
+ * hold anything (NaN included).  A query that sees no key gets o = 0 and
+ * lse = -inf.  P_max == 0 or S_max == 0 (not both): that side is absent and its
+ * pointers may be NULL.  Query head h reads key head h / (H / H_kv).
+ * The sums over keys run in fp32; the weights enter P V in bf16, as in
+ * nc_attention.  Requires D == 128, H % H_kv == 0, H / H_kv <= 128, B % G == 0,
+ * P_max + S_max <= 2^30, strides at least the width they span (NC_ERR_SHAPE);
+ * 16-byte aligned pointers, strides multiples of 8 elements (NC_ERR_ALIGN);
+ * softmax_scale > 0 and finite (NC_ERR_ARG); a workspace of
+ * nc_prefix_attention_workspace_bytes (0 for sizes that need none, or invalid
+ * ones), NC_ERR_WORKSPACE otherwise. */
+size_t nc_prefix_attention_workspace_bytes(int B, int G, int Tq, int H, int Hkv, int P_max, int S_max, int window);
+int nc_prefix_attention(const void* q, long long ldq, const void* k_prefix, const void* v_prefix, long long ldp,
+                        long long lsp, const int32_t* prefix_lens, const void* k_suffix, const void* v_suffix,
+                        long long lds, long long lss, const int32_t* suffix_lens, void* out, float* out_lse_opt, int B,
+                        int G, int Tq, int H, int Hkv, int D, int P_max, int S_max, int window, float softmax_scale,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Clipped policy loss with a KL term, forward and backward, from logits (the
+ * softcapped logits that nc_forward writes, or any others).  For every token t
+ * with a target y_t != -1 ([Math] §Cross-Entropy Loss for lp):
+ *   lp = z_y - logsumexp_v z_v,  r = exp(lp - old_logp),  d = ref_logp - lp,
+ *   L  = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_beta (e^d - d - 1)
+ * weighted by w_t: norm == 0 gives every token 1 / (number of tokens with a
+ * target), norm == 1 every sequence with a target the same weight, shared by
+ * its tokens.
+ *   logits [B*T] rows of V in `dtype` (bf16 or fp32), ldl elements apart;
+ *   targets [B, T] int32 in [0, V) or -1; advantages fp32 [B] or, with
+ *     adv_per_token, [B, T]; old_logp_opt [B, T] fp32, or NULL for lp itself
+ *     (r = 1: the first step on fresh samples); ref_logp_opt [B, T] fp32, or
+ *     NULL for no KL term;
+ *   out_stats [3] fp32: sum w L, sum w (e^d - d - 1), sum w [clipped] (all 0
+ *     when no token has a target);
+ *   out_logp [B, T] fp32: lp, 0 where there is no target;
+ *   out_dlogits_opt [B*T] rows of V in `dtype`, lddl apart, or NULL:
+ *     d(sum w L)/dz = w dL/dlp ([v = y] - softmax(z)_v), 0 in rows without a
+ *     target; a clipped token's ratio term has no gradient, one on the border
+ *     has.  It may be the logits themselves (same pointer and stride); columns
+ *     from V on are neither read nor written.
+ * Row sums and statistics are accumulated in fp32 per thread and fp64 across
+ * threads, in a fixed order.  A target outside [-1, V) sets NC_ERR_DATA and
+ * counts as -1.  -inf logits have probability 0.  NC_ERR_ARG: a missing
+ * pointer, clip_low outside [0, 1), clip_high < 0, kl_beta < 0, norm not 0 or 1;
+ * NC_ERR_SHAPE: B, T or V < 1, a stride below V; NC_ERR_ALIGN: rows not aligned
+ * to their element, workspace not to 16 bytes; NC_ERR_WORKSPACE. */
+size_t nc_policy_loss_workspace_bytes(void);
+int nc_policy_loss(const void* logits, long long ldl, const int32_t* targets, const float* advantages, int adv_per_token,
+                   const float* old_logp_opt, const float* ref_logp_opt, int B, int T, int V, float clip_low,
+                   float clip_high, float kl_beta, int norm, float* out_stats, float* out_logp, void* out_dlogits_opt,
+                   long long lddl, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, read the device status word (an OR of
  * 1 << NC_ERR_DATA and 1 << NC_ERR_TIMEOUT bits set by kernels since the last
  * read), clear it, and return NC_OK, NC_ERR_DATA or NC_ERR_TIMEOUT (timeout
@@ -370,7 +479,8 @@ int nc_set_flag_wait_test(int skew, double wait_limit_ms);
  * it) restarts the count.  Kinds: 0 embed_norm_smear, 1 rmsnorm, 2 rope_table,
  * 3 rope_qknorm, 4 gemm_tcgen05, 5 gemm_cuda_core, 6 attention_tcgen05,
  * 7 attention_cuda_core, 8 ce_combine, 9 ce_rows, 10 loss_mean, 11 last_logits,
- * 12 sample, 13 gemm_tcgen05_bwd, 14 head_bwd_rows, 15 prefix_rmsnorm.
+ * 12 sample, 13 gemm_tcgen05_bwd, 14 head_bwd_rows, 15 prefix_rmsnorm,
+ * 16 qk_norm_rope, 17 prefix_attention, 18 policy_loss.
  * Returns NC_ERR_ARG if events != NULL with kinds == NULL or capacity <= 0. */
 int nc_set_launch_timing(void** events, int* kinds, int capacity, unsigned kind_mask);
 
