@@ -14,20 +14,22 @@
 // per row.  What bounds it: reading the caches from HBM, as long as a key
 // head has fewer than about 250 query rows per group.
 //
-// Work is cut into units, one CTA each:
-//   prefix unit: (group, key head, range of 64-key tiles, 128-row query tile),
-//   suffix unit: (row, key head, range of 64-key tiles, query tile).
-// Every unit leaves its rows' normalised output (fp32) and log-sum-exp in the
-// workspace; k_prefix_combine joins a row's parts with weights
-// exp(lse_part - lse).  A row for which a unit has no visible key gets
-// lse = -inf there.  With one part in all, the unit writes the output itself.
+// The work is a sequence of units, prefix units (group, key head, 128-row query
+// tile) and then suffix units (row, key head, query tile), each a run of
+// 64-key tiles.  The CTAs cut the sequence of all tiles into equal shares, as
+// the lengths in memory give them: a long unit is spread over many CTAs, a CTA
+// takes many short ones, and all finish together.  What a CTA does of a unit is
+// a piece; it leaves its rows' normalised output (fp32) and log-sum-exp in the
+// workspace, at slot (unit + CTA), which no two pieces share.
+// k_prefix_combine joins a row's pieces with weights exp(lse_piece - lse).
 //
-// A CTA: warps 0..3 softmax (one row per thread = TMEM lane; warps without a
-// row sit out), warp 4 TMA, warp 5 MMA.  64-key K and V tiles stream through
-// a ring of 16 KB slots in the order K0 K1 V0 K2 V1 ...; S is double-buffered
-// in TMEM, so Q K_{t+1}^T runs during tile t's exponentials, and P_t (bf16)
-// overwrites the first half of S_t.  Two CTAs share an SM: one's set-up and
-// drain overlap the other's stream.  Every wait is bounded.
+// A CTA: warps 0..3 softmax (one row per thread = TMEM lane), warp 4 cuts the
+// pieces and issues the copies (TMA), warp 5 MMA.  Warp 4 runs ahead: the next
+// pieces' keys stream while the last piece's rows are written.  64-key K and V
+// tiles go through a ring of 16 KB slots in the order K0 K1 V0 K2 V1 ...; S is
+// double-buffered in TMEM, so Q K_{t+1}^T runs during tile t's exponentials,
+// and P_t (bf16) overwrites the first half of S_t.  Two CTAs share an SM.
+// Every wait is bounded.
 #include "nc_internal.cuh"
 #include "ptx.cuh"
 
@@ -45,36 +47,182 @@ constexpr int Q_BOX = kRows * 128;         // 16 KB: 128 rows x 64 columns of Q
 constexpr int KV_BOX = kKeys * 128;        // 8 KB: 64 keys x 64 columns
 constexpr int SLOT_BYTES = 2 * KV_BOX;     // 16 KB
 constexpr int SLOTS = 4;
+constexpr int kPieces = 4;                 // depth of the ring of pieces
+constexpr int kMaxBins = 512;              // entries of either side's table of starts
 constexpr int OFF_SLOT = 2 * Q_BOX;
 constexpr int OFF_BAR = OFF_SLOT + SLOTS * SLOT_BYTES;
-constexpr int SMEM_BYTES = OFF_BAR + 256 + 1024;
+constexpr int OFF_PIECE = OFF_BAR + 256;
+constexpr int OFF_START = OFF_PIECE + kPieces * 64;
+constexpr int SMEM_BYTES = OFF_START + (2 * kMaxBins + 2) * 4 + 1024;
+static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
 constexpr int kThreads = 192, kWarpTma = 4, kWarpMma = 5;
 constexpr uint32_t TMEM_COLS = 256;        // S0 64 | S1 64 | O 128
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.6931471805599453f;
+// What a unit costs besides its tiles (query load, set-up, rows out), in tiles.
+constexpr int kUnitCost = 1;
 
-struct Unit {
-  int suffix;      // 0: prefix keys, 1: a row's own keys
-  int seq, hk;     // group or row, key head
-  int split;
-  int tok0, ntok;  // query tokens of the tile (token = row of the batch * Tq + i)
+struct Piece {
+  int suffix, seq, hk;  // side, group or row, key head
+  int tok0, ntok;       // query tokens (token = row * Tq + i)
+  int lo, hi;           // keys that some row of the unit's sequence sees, from the side's first key
+  int t0, nt;           // key tiles; nt == 0: no more pieces
+  int slot;
+};
+static_assert(sizeof(Piece) <= 64, "piece area");
+
+struct Seq {  // a group's prefix or a row's own keys
+  int P, S;
+  int lo, hi;  // keys that some query sees
 };
 
-__device__ __forceinline__ Unit decode_unit(const PrefixAttnArgs& a, int u) {
-  Unit w;
-  w.suffix = u >= a.units_p;
-  if (w.suffix) u -= a.units_p;
-  const int tiles = w.suffix ? a.tiles_s : a.tiles_p, splits = w.suffix ? a.splits_s : a.splits_p;
-  const int tt = u % tiles;
-  u /= tiles;
-  w.split = u % splits;
-  u /= splits;
-  w.hk = u % a.Hkv;
-  w.seq = u / a.Hkv;
-  const int tokens = (w.suffix ? 1 : a.rows_per_group) * a.Tq, box = w.suffix ? a.box_s : a.box_p;
-  w.tok0 = w.seq * tokens + tt * box;
-  w.ntok = min(box, tokens - tt * box);
-  return w;
+__device__ __forceinline__ int clamp_len(int n, int most) { return min(max(n, 0), most); }
+
+// Keys [lo, hi) of group g's prefix that a query of one of its rows sees.  All
+// lanes of the warp together: a window makes lo depend on the shortest row.
+__device__ __forceinline__ Seq prefix_seq(const PrefixAttnArgs& a, int g, int lane) {
+  Seq s;
+  s.P = s.hi = clamp_len(a.prefix_lens[g], a.P_max);
+  s.S = s.lo = 0;
+  if (a.window < a.P_max + a.S_max) {
+    int least = a.S_max;
+    if (a.S_max > 0) {
+      for (int r = lane; r < a.rows_per_group; r += 32)
+        least = min(least, clamp_len(a.suffix_lens[g * a.rows_per_group + r], a.S_max));
+      least = __reduce_min_sync(0xffffffffu, least);
+    }
+    s.lo = min(s.P, max(0, s.P + least - a.Tq - a.window + 1));
+  }
+  return s;
+}
+
+__device__ __forceinline__ Seq suffix_seq(const PrefixAttnArgs& a, int b) {
+  Seq s;
+  s.P = a.P_max > 0 ? clamp_len(a.prefix_lens[b / a.rows_per_group], a.P_max) : 0;
+  s.S = s.hi = clamp_len(a.suffix_lens[b], a.S_max);
+  s.lo = min(s.S, max(0, s.S - a.Tq - a.window + 1));
+  return s;
+}
+
+// first key and number of key tiles of a sequence's query tile tt (prefix:
+// every tile has the same; suffix: keys behind the tile's last query are not
+// its own)
+__device__ __forceinline__ int unit_tiles(const PrefixAttnArgs& a, const Seq& s, int suffix, int tt, int* t0) {
+  int lo = s.lo, hi = s.hi;
+  if (suffix) {
+    const int first = s.S - a.Tq + tt * a.box_s, last = s.S - a.Tq + min(a.Tq, (tt + 1) * a.box_s) - 1;
+    lo = max(lo, first - a.window + 1);
+    hi = min(hi, last + 1);
+  }
+  *t0 = lo / kKeys;
+  return lo < hi ? (hi + kKeys - 1) / kKeys - *t0 : 0;
+}
+
+__device__ __forceinline__ int unit_cost(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
+
+// cost of all query tiles of a row, for one key head
+__device__ __forceinline__ int suffix_cost(const PrefixAttnArgs& a, const Seq& s) {
+  int c = 0, t0;
+  for (int tt = 0; tt < a.tiles_s; ++tt) c += unit_cost(unit_tiles(a, s, 1, tt, &t0));
+  return c;
+}
+
+// Fills the tables of starts (cost before each bin of groups, then of rows;
+// the last entry is the total).  All threads of the CTA.
+__device__ void fill_starts(const PrefixAttnArgs& a, int* start, int warp, int lane) {
+  for (int i = warp; i < a.bins_p; i += kThreads / 32) {
+    int c = 0, t0;
+    for (int g = i * a.bin_p; g < min(a.G, (i + 1) * a.bin_p); ++g)
+      c += a.Hkv * a.tiles_p * unit_cost(unit_tiles(a, prefix_seq(a, g, lane), 0, 0, &t0));
+    if (lane == 0) start[i] = c;
+  }
+  for (int i = threadIdx.x; i < a.bins_s; i += kThreads) {
+    int c = 0;
+    for (int b = i * a.bin_s; b < min(a.B, (i + 1) * a.bin_s); ++b) c += a.Hkv * suffix_cost(a, suffix_seq(a, b));
+    start[a.bins_p + i] = c;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int n = a.bins_p + a.bins_s, per = (n + 31) / 32, i0 = min(n, lane * per), i1 = min(n, i0 + per);
+    int sum = 0;
+    for (int i = i0; i < i1; ++i) sum += start[i];
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    const int total = __shfl_sync(0xffffffffu, before, 31);
+    before -= sum;
+    for (int i = i0; i < i1; ++i) {
+      const int v = start[i];
+      start[i] = before;
+      before += v;
+    }
+    if (lane == 0) start[n] = total;
+  }
+  __syncthreads();
+}
+
+// share of the total cost that a CTA takes
+__device__ __forceinline__ int share_of(const PrefixAttnArgs& a, int total) {
+  return max((total + a.ctas - 1) / a.ctas, kUnitCost + 1);
+}
+
+// The piece that holds cost position v, as far as `end`; *next: the position
+// behind it.  A piece may have no tile (it holds only a unit's fixed cost).
+// All lanes of a warp together.  Lengths that change while the kernel runs give
+// wrong pieces, but every loop ends and every index stays in range.
+__device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, int v, int end, int lane, int* next) {
+  int lo = 0, hi = a.bins_p + a.bins_s;  // the last bin that starts at or before v
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (start[mid] <= v) lo = mid; else hi = mid;
+  }
+  Piece p;
+  p.suffix = lo >= a.bins_p;
+  int at = v - start[lo], t0 = 0, tiles = 0, tt = 0;
+  Seq s;
+  if (!p.suffix) {
+    for (p.seq = lo * a.bin_p;; ++p.seq) {
+      s = prefix_seq(a, p.seq, lane);
+      tiles = unit_tiles(a, s, 0, 0, &t0);
+      const int all = a.Hkv * a.tiles_p * unit_cost(tiles);
+      if (at < all || p.seq + 1 >= a.G) break;
+      at -= all;
+    }
+    const int u = min(at / max(unit_cost(tiles), 1), a.Hkv * a.tiles_p - 1);
+    at -= u * unit_cost(tiles);
+    p.hk = u / a.tiles_p;
+    tt = u % a.tiles_p;
+  } else {
+    int one;
+    for (p.seq = (lo - a.bins_p) * a.bin_s;; ++p.seq) {
+      s = suffix_seq(a, p.seq);
+      one = suffix_cost(a, s);
+      if (at < a.Hkv * one || p.seq + 1 >= a.B) break;
+      at -= a.Hkv * one;
+    }
+    p.hk = min(at / max(one, 1), a.Hkv - 1);
+    at -= p.hk * one;
+    for (tt = 0;; ++tt) {
+      tiles = unit_tiles(a, s, 1, tt, &t0);
+      if (at < unit_cost(tiles) || tt + 1 >= a.tiles_s) break;
+      at -= unit_cost(tiles);
+    }
+  }
+  const int unit_end = v - at + unit_cost(tiles);
+  *next = max(v + 1, min(end, unit_end));
+  const int first = max(0, at - kUnitCost), last = *next - (v - at) - kUnitCost;
+  p.t0 = t0 + first;
+  p.nt = min(max(0, last - first), max(0, tiles - first));
+  p.lo = s.lo;
+  p.hi = s.hi;
+  const int tokens = (p.suffix ? 1 : a.rows_per_group) * a.Tq, box = p.suffix ? a.box_s : a.box_p;
+  p.tok0 = p.seq * tokens + tt * box;
+  p.ntok = min(box, tokens - tt * box);
+  p.slot = (p.seq * a.Hkv + p.hk) * (p.suffix ? a.tiles_s : a.tiles_p) + tt + blockIdx.x;
+  return p;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -91,91 +239,60 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-  enum { B_Q = 0, B_F = 1, B_E = B_F + SLOTS, B_S = B_E + SLOTS, B_P = B_S + 2, B_O = B_P + 2, B_FIN, B_DONE, NB };
-  static_assert(NB * 8 + 8 + 32 <= 256, "barrier area");
+  enum {
+    B_QF = 0, B_QE, B_F, B_E = B_F + SLOTS, B_S = B_E + SLOTS, B_P = B_S + 2, B_O = B_P + 2, B_FIN, B_OE, B_DF,
+    B_DE = B_DF + kPieces, B_DONE = B_DE + kPieces, NB
+  };
+  static_assert(NB * 8 + 8 <= 256, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NB);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* s_range = reinterpret_cast<int*>(tmem_slot + 2);  // lo of warps 0..3, hi of warps 0..3
+  auto piece_mem = [&](int i) { return reinterpret_cast<Piece*>(smem + OFF_PIECE + (i % kPieces) * 64); };
+  int* start = reinterpret_cast<int*>(smem + OFF_START);
   const uint32_t bar0 = ptx::smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Unit w = decode_unit(a, blockIdx.x);
-  const int R = a.H / a.Hkv;
-  const int nrows = w.ntok * R, nwarps = (nrows + 31) / 32;
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(bar(B_Q), 1);
+    ptx::mbar_init(bar(B_QF), 1);
+    ptx::mbar_init(bar(B_QE), 1);
     for (int s = 0; s < SLOTS; ++s) {
       ptx::mbar_init(bar(B_F + s), 1);
       ptx::mbar_init(bar(B_E + s), 1);
     }
     for (int g = 0; g < 2; ++g) {
       ptx::mbar_init(bar(B_S + g), 1);
-      ptx::mbar_init(bar(B_P + g), nwarps);
+      ptx::mbar_init(bar(B_P + g), 4);
     }
     ptx::mbar_init(bar(B_O), 1);
     ptx::mbar_init(bar(B_FIN), 1);
+    ptx::mbar_init(bar(B_OE), 4);
+    for (int i = 0; i < kPieces; ++i) {
+      ptx::mbar_init(bar(B_DF + i), 1);
+      ptx::mbar_init(bar(B_DE + i), 5);  // four softmax warps and the MMA thread
+    }
     ptx::mbar_init(bar(B_DONE), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
+  if (warp == kWarpTma && lane < 6)
+    ptx::prefetch_tmap(lane == 0 ? &tmQp : lane == 1 ? &tmQs : lane == 2 ? &tmKp : lane == 3 ? &tmVp : lane == 4 ? &tmKs : &tmVs);
   pdl_wait();  // lengths, q and the caches may come from the previous kernel
-
-  // Visible keys of each row among the unit's keys: [lo, hi), counted from the
-  // first key of the prefix or of the row's own keys.
-  int lo = 0, hi = 0;
-  const int token = w.tok0 + (int)threadIdx.x / R;
-  if (warp < 4) {
-    if ((int)threadIdx.x < nrows) {
-      const int b = token / a.Tq, g = b / a.rows_per_group;
-      int P = a.prefix_lens != nullptr ? a.prefix_lens[g] : 0, S = a.suffix_lens != nullptr ? a.suffix_lens[b] : 0;
-      if (P < 0 || P > a.P_max || S < 0 || S > a.S_max) {
-        atomicOr(a.status, kStatusData);
-        P = min(max(P, 0), a.P_max);
-        S = min(max(S, 0), a.S_max);
-      }
-      const int pos = P + S - a.Tq + token % a.Tq;
-      const int base = w.suffix ? P : 0;
-      lo = max(0, pos - a.window + 1 - base);
-      hi = min(w.suffix ? S : P, pos + 1 - base);
-      if (lo >= hi) lo = hi = 0;
-    }
-    const int l = __reduce_min_sync(0xffffffffu, lo < hi ? lo : 0x7fffffff);
-    const int h = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-      s_range[warp] = l;
-      s_range[4 + warp] = h;
-    }
+  fill_starts(a, start, warp, lane);
+  const int bins = a.bins_p + a.bins_s, total = start[bins];
+  if (blockIdx.x == 0) {  // for the joining kernel; lengths out of range are reported once
+    for (int i = threadIdx.x; i <= bins; i += kThreads) a.starts[i] = start[i];
+    bool bad = false;
+    if (a.P_max > 0)
+      for (int g = threadIdx.x; g < a.G; g += kThreads) bad |= (unsigned)a.prefix_lens[g] > (unsigned)a.P_max;
+    if (a.S_max > 0)
+      for (int b = threadIdx.x; b < a.B; b += kThreads) bad |= (unsigned)a.suffix_lens[b] > (unsigned)a.S_max;
+    if (bad) atomicOr(a.status, kStatusData);
   }
-  __syncthreads();
-  const int ulo = min(min(s_range[0], s_range[1]), min(s_range[2], s_range[3]));
-  const int uhi = max(max(s_range[4], s_range[5]), max(s_range[6], s_range[7]));
-  int nt = 0, t0 = 0;
-  if (ulo < uhi) {
-    const int first = ulo / kKeys, tiles = (uhi + kKeys - 1) / kKeys - first;
-    const int splits = w.suffix ? a.splits_s : a.splits_p;
-    const int chunk = max(a.min_tiles, (tiles + splits - 1) / splits);
-    t0 = first + w.split * chunk;
-    nt = min(chunk, tiles - w.split * chunk);
-  }
-  const int part = w.suffix ? a.splits_p + w.split : w.split;
-  const bool direct = a.splits_p + a.splits_s == 1;
-  const long long total_rows = (long long)a.B * a.Tq * a.H;
-  // row of the outputs: token-major, then head
-  const long long orow = (long long)token * a.H + w.hk * R + (int)threadIdx.x % R;
-  if (nt <= 0) {
-    if ((int)threadIdx.x < nrows) {
-      if (direct) {
-        uint4* d = reinterpret_cast<uint4*>(a.out + orow * kD);
-        for (int i = 0; i < kD / 8; ++i) d[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (a.out_lse != nullptr) a.out_lse[orow] = -INFINITY;
-      } else {
-        a.part_lse[(long long)part * total_rows + orow] = -INFINITY;
-      }
-    }
-    return;
-  }
+  const int share = share_of(a, total);
+  const long long v_begin = (long long)blockIdx.x * share;
+  if (v_begin >= total) return;
+  const int v0 = (int)v_begin, v1 = (int)min(v_begin + share, (long long)total);
   if (warp == kWarpMma) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
     ptx::tmem_relinquish();
@@ -186,41 +303,77 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = *tmem_slot;
   auto sSlot = [&](int s) { return ptx::smem_u32(smem + OFF_SLOT + s * SLOT_BYTES); };
   const uint32_t sQ = ptx::smem_u32(smem);
-  // place in the ring's sequence of K_t and V_t
+  const int R = a.H / a.Hkv;
+  // place of a piece's K_t and V_t in its sequence of 2 nt tiles
   auto seq_k = [](int t) { return t == 0 ? 0 : 2 * t - 1; };
-  auto seq_v = [&](int t) { return t + 1 < nt ? 2 * t + 2 : 2 * nt - 1; };
+  auto seq_v = [](int t, int nt) { return t + 1 < nt ? 2 * t + 2 : 2 * nt - 1; };
+  // the n-th piece; false on a timeout
+  auto piece_wait = [&](int n, Piece* p) -> bool {
+    if (*abort_flag || !ptx::mbar_wait(bar(B_DF + n % kPieces), (uint32_t)(n / kPieces) & 1u, a.status)) return false;
+    *p = *piece_mem(n);
+    return true;
+  };
 
   if (warp == kWarpTma) {
-    if (ptx::elect_one()) {
-      const void* tq = w.suffix ? (const void*)&tmQs : (const void*)&tmQp;
-      const void* tk = w.suffix ? (const void*)&tmKs : (const void*)&tmKp;
-      const void* tv = w.suffix ? (const void*)&tmVs : (const void*)&tmVp;
-      const int box_tok = w.suffix ? a.box_s : a.box_p;
-      ptx::mbar_arrive_expect_tx(bar(B_Q), (uint32_t)(2 * box_tok * R * 128));
-      ptx::tma_load_4d(sQ, tq, bar(B_Q), 0, w.hk * R, w.tok0, 0);
-      ptx::tma_load_4d(sQ + Q_BOX, tq, bar(B_Q), 64, w.hk * R, w.tok0, 0);
-      bool ok = true;
-      int issued = 0;
-      for (int sc = 0; sc < 2 * nt; ++sc) {
-        // K0 K1 V0 K2 V1 ... K_{nt-1} V_{nt-2} V_{nt-1}
-        const bool is_k = sc == 0 || (sc % 2 == 1 && sc < 2 * nt - 1);
-        const int t = sc == 0 ? 0 : (is_k ? (sc + 1) / 2 : (sc == 2 * nt - 1 ? nt - 1 : sc / 2 - 1));
-        const int s = sc % SLOTS;
-        const uint32_t ph = (uint32_t)(sc / SLOTS) & 1u;
-        if (*abort_flag || !ptx::mbar_wait(bar(B_E + s), ph ^ 1, a.status)) {
-          ok = false;
-          break;
-        }
-        ptx::mbar_arrive_expect_tx(bar(B_F + s), SLOT_BYTES);
-        const int key = (t0 + t) * kKeys;
-        ptx::tma_load_4d(sSlot(s), is_k ? tk : tv, bar(B_F + s), 0, w.hk, key, w.seq);
-        ptx::tma_load_4d(sSlot(s) + KV_BOX, is_k ? tk : tv, bar(B_F + s), 64, w.hk, key, w.seq);
-        ++issued;
+    bool ok = true;
+    int sc0 = 0, n = 0;           // tiles issued by earlier pieces, pieces
+    int sc_done = 0, q_done = 0;  // lane 0: copies issued
+    int v = v0;
+    while (ok) {
+      Piece p;
+      p.nt = 0;
+      while (v < v1 && p.nt == 0) {
+        int next;
+        p = piece_at(a, start, v, v1, lane, &next);
+        v = next;
       }
+      if (lane == 0) {
+        ok = !*abort_flag && ptx::mbar_wait(bar(B_DE + n % kPieces), ((uint32_t)(n / kPieces) & 1u) ^ 1u, a.status);
+        if (ok) {
+          *piece_mem(n) = p;
+          ptx::mbar_arrive(bar(B_DF + n % kPieces));
+          const void* tq = p.suffix ? (const void*)&tmQs : (const void*)&tmQp;
+          const void* tk = p.suffix ? (const void*)&tmKs : (const void*)&tmKp;
+          const void* tv = p.suffix ? (const void*)&tmVs : (const void*)&tmVp;
+          for (int i = 0; ok && i < 2 * p.nt; ++i) {
+            // K0 K1 V0 K2 V1 ... K_{nt-1} V_{nt-2} V_{nt-1}
+            const bool is_k = i == 0 || (i % 2 == 1 && i < 2 * p.nt - 1);
+            const int t = i == 0 ? 0 : (is_k ? (i + 1) / 2 : (i == 2 * p.nt - 1 ? p.nt - 1 : i / 2 - 1));
+            const int s = (sc0 + i) % SLOTS;
+            if (*abort_flag || !ptx::mbar_wait(bar(B_E + s), ((uint32_t)((sc0 + i) / SLOTS) & 1u) ^ 1u, a.status)) {
+              ok = false;
+              break;
+            }
+            ptx::mbar_arrive_expect_tx(bar(B_F + s), SLOT_BYTES);
+            const int key = (p.t0 + t) * kKeys;
+            ptx::tma_load_4d(sSlot(s), is_k ? tk : tv, bar(B_F + s), 0, p.hk, key, p.seq);
+            ptx::tma_load_4d(sSlot(s) + KV_BOX, is_k ? tk : tv, bar(B_F + s), 64, p.hk, key, p.seq);
+            ++sc_done;
+            if (i == 0) {
+              // the first keys do not need the query buffer, which the last
+              // piece's products may still be reading
+              if (*abort_flag || !ptx::mbar_wait(bar(B_QE), ((uint32_t)n & 1u) ^ 1u, a.status)) {
+                ok = false;
+                break;
+              }
+              ptx::mbar_arrive_expect_tx(bar(B_QF), (uint32_t)(2 * (p.suffix ? a.box_s : a.box_p) * R * 128));
+              ptx::tma_load_4d(sQ, tq, bar(B_QF), 0, p.hk * R, p.tok0, 0);
+              ptx::tma_load_4d(sQ + Q_BOX, tq, bar(B_QF), 64, p.hk * R, p.tok0, 0);
+              ++q_done;
+            }
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      sc0 += 2 * p.nt;
+      ++n;
+      if (p.nt == 0) break;
+    }
+    if (lane == 0) {
       if (!ok) *abort_flag = 1;
       // every copy issued here has landed before the CTA may exit
-      ptx::mbar_wait(bar(B_Q), 0, a.status);
-      for (int sc = max(0, issued - SLOTS); sc < issued; ++sc)
+      if (q_done > 0) ptx::mbar_wait(bar(B_QF), (uint32_t)(q_done - 1) & 1u, a.status);
+      for (int sc = max(0, sc_done - SLOTS); sc < sc_done; ++sc)
         ptx::mbar_wait(bar(B_F + sc % SLOTS), (uint32_t)(sc / SLOTS) & 1u, a.status);
     }
   } else if (warp == kWarpMma) {
@@ -232,192 +385,225 @@ __global__ void __launch_bounds__(kThreads, 2)
       auto full = [&](int sc) -> bool {
         return !*abort_flag && ptx::mbar_wait(bar(B_F + sc % SLOTS), (uint32_t)(sc / SLOTS) & 1u, a.status);
       };
-      auto qk = [&](int t) -> bool {
-        const int sc = seq_k(t);
-        if (!full(sc)) return false;
-        ptx::tc_fence_after();
-        const uint64_t dk = dk0 + (uint64_t)((sc % SLOTS) * (SLOT_BYTES >> 4));
-#pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk)
-          ptx::mma_bf16_ss(tmem + (uint32_t)((t & 1) * kKeys), dq + (uint64_t)((kk >> 2) * (Q_BOX >> 4) + (kk & 3) * 2),
-                           dk + (uint64_t)((kk >> 2) * (KV_BOX >> 4) + (kk & 3) * 2), idesc_qk, kk > 0 ? 1u : 0u);
-        ptx::mma_commit(bar(B_S + (t & 1)));
-        ptx::mma_commit(bar(B_E + sc % SLOTS));
-        return true;
-      };
-      bool ok = ptx::mbar_wait(bar(B_Q), 0, a.status) && qk(0);
-      for (int t = 0; ok && t < nt; ++t) {
-        // S_{t+1} goes where P_{t-1} was, whose product was issued before
-        if (t + 1 < nt && !qk(t + 1)) {
+      bool ok = true;
+      int sc0 = 0, j0 = 0;  // ring tiles and key tiles of earlier pieces
+      for (int n = 0;; ++n) {
+        Piece p;
+        if (!piece_wait(n, &p)) {
           ok = false;
           break;
         }
-        const int sc = seq_v(t);
-        if (!full(sc) || *abort_flag || !ptx::mbar_wait(bar(B_P + (t & 1)), (uint32_t)(t >> 1) & 1u, a.status)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint64_t dv = dv0 + (uint64_t)((sc % SLOTS) * (SLOT_BYTES >> 4));
+        ptx::mbar_arrive(bar(B_DE + n % kPieces));
+        if (p.nt == 0) break;
+        auto qk = [&](int t) -> bool {
+          const int sc = sc0 + seq_k(t), j = j0 + t;
+          if (!full(sc)) return false;
+          ptx::tc_fence_after();
+          const uint64_t dk = dk0 + (uint64_t)((sc % SLOTS) * (SLOT_BYTES >> 4));
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          ptx::mma_bf16_ts(tmem + 128u, tmem + (uint32_t)((t & 1) * kKeys + kk * 8), dv + (uint64_t)(kk * (2048 >> 4)),
-                           idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
-        ptx::mma_commit(bar(B_E + sc % SLOTS));
-        // the softmax waits for B_O only where S_t shows that phase t - 2 is over;
-        // the last product has a barrier of its own
-        ptx::mma_commit(bar(t + 1 < nt ? B_O : B_FIN));
+          for (int kk = 0; kk < kD / 16; ++kk)
+            ptx::mma_bf16_ss(tmem + (uint32_t)((j & 1) * kKeys), dq + (uint64_t)((kk >> 2) * (Q_BOX >> 4) + (kk & 3) * 2),
+                             dk + (uint64_t)((kk >> 2) * (KV_BOX >> 4) + (kk & 3) * 2), idesc_qk, kk > 0 ? 1u : 0u);
+          ptx::mma_commit(bar(B_S + (j & 1)));
+          ptx::mma_commit(bar(B_E + sc % SLOTS));
+          if (t + 1 == p.nt) ptx::mma_commit(bar(B_QE));
+          return true;
+        };
+        ok = ptx::mbar_wait(bar(B_QF), (uint32_t)n & 1u, a.status) && qk(0);
+        for (int t = 0; ok && t < p.nt; ++t) {
+          // S_{t+1} goes where P_{t-1} was, whose product was issued before
+          if (t + 1 < p.nt && !qk(t + 1)) {
+            ok = false;
+            break;
+          }
+          const int sc = sc0 + seq_v(t, p.nt), j = j0 + t;
+          if (!full(sc) || *abort_flag || !ptx::mbar_wait(bar(B_P + (j & 1)), (uint32_t)(j >> 1) & 1u, a.status)) {
+            ok = false;
+            break;
+          }
+          // the last piece's rows have been read out of O
+          if (t == 0 && n > 0 && !ptx::mbar_wait(bar(B_OE), (uint32_t)(n - 1) & 1u, a.status)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint64_t dv = dv0 + (uint64_t)((sc % SLOTS) * (SLOT_BYTES >> 4));
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            ptx::mma_bf16_ts(tmem + 128u, tmem + (uint32_t)((j & 1) * kKeys + kk * 8), dv + (uint64_t)(kk * (2048 >> 4)),
+                             idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
+          ptx::mma_commit(bar(B_E + sc % SLOTS));
+          ptx::mma_commit(bar(B_O));
+          if (t + 1 == p.nt) ptx::mma_commit(bar(B_FIN));
+        }
+        if (!ok) break;
+        sc0 += 2 * p.nt;
+        j0 += p.nt;
       }
       if (!ok) *abort_flag = 1;
       ptx::mma_commit(bar(B_DONE));
       ptx::mbar_wait(bar(B_DONE), 0, a.status);
     }
-  } else if (warp < nwarps) {
+  } else {
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const uint32_t tO = tmem + 128u + lane_off;
     const float c = a.scale_log2;
-    float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
-    for (int t = 0; t < nt; ++t) {
-      const uint32_t tS = tmem + (uint32_t)((t & 1) * kKeys) + lane_off;
-      const int k0 = (t0 + t) * kKeys;
-      const int clo = lo - k0, chi = hi - k0;  // visible columns [clo, chi)
-      if (*abort_flag || !ptx::mbar_wait(bar(B_S + (t & 1)), (uint32_t)(t >> 1) & 1u, a.status)) {
+    int sc0 = 0, j0 = 0;
+    for (int n = 0; ok; ++n) {
+      Piece p;
+      if (!piece_wait(n, &p)) {
         ok = false;
         break;
       }
-      ptx::tc_fence_after();
-      float x[kKeys];
-      {
-        uint32_t u0[32], u1[32];
-        ptx::tmem_ld32(tS, u0);
-        ptx::tmem_ld32(tS + 32, u1);
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          x[i] = __uint_as_float(u0[i]);
-          x[32 + i] = __uint_as_float(u1[i]);
-        }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(B_DE + n % kPieces));
+      if (p.nt == 0) break;
+      const int nrows = p.ntok * R;
+      const bool live = (int)threadIdx.x < nrows, warp_live = warp * 32 < nrows;
+      // keys [lo, hi) that this row sees, from the side's first key
+      int lo = 0, hi = 0;
+      const int token = p.tok0 + (int)threadIdx.x / R;
+      if (live) {
+        const int b = token / a.Tq;
+        const int P = a.P_max > 0 ? clamp_len(a.prefix_lens[b / a.rows_per_group], a.P_max) : 0;
+        const int S = a.S_max > 0 ? clamp_len(a.suffix_lens[b], a.S_max) : 0;
+        const int pos = P + S - a.Tq + token % a.Tq, base = p.suffix ? P : 0;
+        lo = max(0, pos - a.window + 1 - base);
+        hi = min(p.suffix ? S : P, pos + 1 - base);
+        if (lo >= hi) lo = hi = 0;
       }
-      if (!__all_sync(0xffffffffu, clo <= 0 && chi >= kKeys)) {
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) x[i] = (i >= clo && i < chi) ? x[i] : -INFINITY;
-      }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int i = 4; i < kKeys; i += 4)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[i + k]);
-      const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      // the running max moves only when it grows by more than 2^8
-      const bool rescale = (tmax - m_run) * c > kRescaleThreshold;
-      const float m_new = rescale ? tmax : m_run;
-      const float mc = m_new == -INFINITY ? 0.f : m_new * c;
-      uint32_t pk[32];
-      float2 sm[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 e = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), c2, mc2);
-        const float2 p = make_float2(ex2(e.x), ex2(e.y));
-        sm[i & 1] = __fadd2_rn(sm[i & 1], p);
-        pk[i] = pack_bf16(p.x, p.y);
-      }
-      ptx::tmem_st32(tS, pk);
-      const float alpha = rescale ? ex2(m_run * c - mc) : 1.f;  // 0 when m_run == -inf
-      if (rescale) {
-        l_run *= alpha;
-        m_run = m_new;
-      }
-      const float2 s2 = __fadd2_rn(sm[0], sm[1]);
-      l_run += s2.x + s2.y;
-      // P V of tile t - 1 must have landed before O is rescaled
-      if (t > 0 && __any_sync(0xffffffffu, rescale)) {
-        if (!ptx::mbar_wait(bar(B_O), (uint32_t)(t - 1) & 1u, a.status)) {
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int t = 0; t < p.nt; ++t) {
+        const int j = j0 + t;
+        const uint32_t tS = tmem + (uint32_t)((j & 1) * kKeys) + lane_off;
+        const int k0 = (p.t0 + t) * kKeys;
+        if (*abort_flag || !ptx::mbar_wait(bar(B_S + (j & 1)), (uint32_t)(j >> 1) & 1u, a.status)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
+        if (warp_live) {
+          const int clo = lo - k0, chi = hi - k0;  // visible columns [clo, chi)
+          float x[kKeys];
+          {
+            uint32_t u0[32], u1[32];
+            ptx::tmem_ld32(tS, u0);
+            ptx::tmem_ld32(tS + 32, u1);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              x[i] = __uint_as_float(u0[i]);
+              x[32 + i] = __uint_as_float(u1[i]);
+            }
+          }
+          if (!__all_sync(0xffffffffu, clo <= 0 && chi >= kKeys)) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) x[i] = (i >= clo && i < chi) ? x[i] : -INFINITY;
+          }
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < kKeys; i += 4)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[i + k]);
+          const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // the running max moves only when it grows by more than 2^8
+          const bool rescale = (tmax - m_run) * c > kRescaleThreshold;
+          const float m_new = rescale ? tmax : m_run;
+          const float mc = m_new == -INFINITY ? 0.f : m_new * c;
+          uint32_t pk[32];
+          float2 sm[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 e = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), c2, mc2);
+            const float2 q = make_float2(ex2(e.x), ex2(e.y));
+            sm[i & 1] = __fadd2_rn(sm[i & 1], q);
+            pk[i] = pack_bf16(q.x, q.y);
+          }
+          ptx::tmem_st32(tS, pk);
+          const float alpha = rescale ? ex2(m_run * c - mc) : 1.f;  // 0 when m_run == -inf
+          if (rescale) {
+            l_run *= alpha;
+            m_run = m_new;
+          }
+          const float2 s2 = __fadd2_rn(sm[0], sm[1]);
+          l_run += s2.x + s2.y;
+          // P V of tile t - 1 must have landed before O is rescaled (S_t shows
+          // that the one before it has)
+          if (t > 0 && __any_sync(0xffffffffu, rescale)) {
+            if (!ptx::mbar_wait(bar(B_O), (uint32_t)(j - 1) & 1u, a.status)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t u[32];
+              ptx::tmem_ld32(tO + (uint32_t)(cc * 32), u);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
+              ptx::tmem_st32(tO + (uint32_t)(cc * 32), u);
+            }
+          }
+        }
+        // V rows that no query of the sequence sees (behind the end, before
+        // the window) may hold anything: they become zeros, since 0 x NaN is not 0
+        if (k0 < p.lo || k0 + kKeys > p.hi) {
+          const int sc = sc0 + seq_v(t, p.nt), s = sc % SLOTS;
+          if (!ptx::mbar_wait(bar(B_F + s), (uint32_t)(sc / SLOTS) & 1u, a.status)) {
+            ok = false;
+            break;
+          }
+          for (int i = threadIdx.x; i < kKeys * 16; i += 128) {
+            const int key = k0 + i / 16;
+            if (key < p.lo || key >= p.hi)
+              *reinterpret_cast<uint4*>(smem + OFF_SLOT + s * SLOT_BYTES + ((i & 8) ? KV_BOX : 0) + (i / 16) * 128 +
+                                        (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(B_P + (j & 1)));
+      }
+      if (!ok || !ptx::mbar_wait(bar(B_FIN), (uint32_t)n & 1u, a.status)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      if (warp_live) {
+        const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
+        const long long prow = (long long)p.slot * ((p.suffix ? a.box_s : a.box_p) * R) + threadIdx.x;
+        float* dst = (p.suffix ? a.part_os : a.part_op) + prow * kD;
 #pragma unroll 1
         for (int cc = 0; cc < 4; ++cc) {
           uint32_t u[32];
           ptx::tmem_ld32(tO + (uint32_t)(cc * 32), u);
           ptx::tmem_ld_wait();
+          if (live && inv != 0.f) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
-          ptx::tmem_st32(tO + (uint32_t)(cc * 32), u);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(u[8 * q + e]) * inv);
+              ptx::st_global_v8(dst + 32 * cc + 8 * q, w);
+            }
+          }
         }
+        // a row that sees none of the piece's keys has weight 0 and no output there
+        if (live)
+          (p.suffix ? a.part_ls : a.part_lp)[prow] = inv != 0.f ? (m_run * c + log2f(l_run)) * kLn2 : -INFINITY;
       }
-      // V rows that no row of the unit sees (behind the end, before the
-      // window) may hold anything: they become zeros, since 0 x NaN is not 0
-      if (k0 < ulo || k0 + kKeys > uhi) {
-        const int sc = seq_v(t), s = sc % SLOTS;
-        if (!ptx::mbar_wait(bar(B_F + s), (uint32_t)(sc / SLOTS) & 1u, a.status)) {
-          ok = false;
-          break;
-        }
-        for (int i = threadIdx.x; i < kKeys * 16; i += 32 * nwarps) {
-          const int key = k0 + i / 16;
-          if (key < ulo || key >= uhi)
-            *reinterpret_cast<uint4*>(smem + OFF_SLOT + s * SLOT_BYTES + ((i & 8) ? KV_BOX : 0) + (i / 16) * 128 + (i & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
-        ptx::fence_proxy_async_smem();
-      }
-      ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(B_P + (t & 1)));
+      if (lane == 0) ptx::mbar_arrive(bar(B_OE));
+      sc0 += 2 * p.nt;
+      j0 += p.nt;
     }
-    if (ok && ptx::mbar_wait(bar(B_FIN), 0, a.status)) {
-      ptx::tc_fence_after();
-      const bool live = (int)threadIdx.x < nrows;
-      const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
-      const float lse = l_run > 0.f ? (m_run * c + log2f(l_run)) * kLn2 : -INFINITY;
-      const long long prow = (long long)part * total_rows + orow;
-#pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {
-        uint32_t u[32];
-        ptx::tmem_ld32(tO + (uint32_t)(cc * 32), u);
-        ptx::tmem_ld_wait();
-        if (!live) continue;
-        // a row whose keys are all masked in this unit: its accumulator holds
-        // nothing of its own
-        if (inv == 0.f) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) u[i] = 0u;
-        }
-        if (direct) {
-          uint4* d = reinterpret_cast<uint4*>(a.out + orow * kD) + 4 * cc;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = pack_bf16(__uint_as_float(u[8 * q + 2 * e]) * inv, __uint_as_float(u[8 * q + 2 * e + 1]) * inv);
-            d[q] = make_uint4(v[0], v[1], v[2], v[3]);
-          }
-        } else {
-          float* d = a.part_o + prow * kD + 32 * cc;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(u[8 * q + e]) * inv);
-            ptx::st_global_v8(d + 8 * q, v);
-          }
-        }
-      }
-      if (live) {
-        if (!direct)
-          a.part_lse[prow] = lse;
-        else if (a.out_lse != nullptr)
-          a.out_lse[orow] = lse;
-      }
-      ptx::tc_fence_before();
-    } else {
-      *abort_flag = 1;
-    }
+    if (!ok) *abort_flag = 1;
   }
   __syncthreads();
   if (warp == kWarpMma) {
@@ -426,33 +612,71 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Joins the parts of a row: one warp per row, four columns per lane.
+// Joins a row's pieces: one warp per row, four columns per lane.
 __global__ void __launch_bounds__(128) k_prefix_combine(const PrefixAttnArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long rows = (long long)a.B * a.Tq * a.H;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);  // token-major, then head
   const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const int parts = a.splits_p + a.splits_s;
+  if (row >= (long long)a.B * a.Tq * a.H) return;
+  const int R = a.H / a.Hkv, token = (int)(row / a.H), h = (int)(row % a.H), hk = h / R;
+  const int share = share_of(a, a.starts[a.bins_p + a.bins_s]);
+  // the row's pieces on either side: slots [first, first + count) and its row in each
+  long long first[2] = {0, 0};
+  int count[2] = {0, 0}, tr[2] = {0, 0};
+  if (a.P_max > 0) {
+    const int g = token / (a.rows_per_group * a.Tq), it = token % (a.rows_per_group * a.Tq), tt = it / a.box_p;
+    int at = a.starts[g / a.bin_p], t0;
+    for (int i = g / a.bin_p * a.bin_p; i < g; ++i)
+      at += a.Hkv * a.tiles_p * unit_cost(unit_tiles(a, prefix_seq(a, i, lane), 0, 0, &t0));
+    const int tiles = unit_tiles(a, prefix_seq(a, g, lane), 0, 0, &t0);
+    at += (hk * a.tiles_p + tt) * unit_cost(tiles) + kUnitCost;
+    if (tiles > 0) {
+      first[0] = (g * a.Hkv + hk) * a.tiles_p + tt + at / share;
+      count[0] = (at + tiles - 1) / share - at / share + 1;
+    }
+    tr[0] = it % a.box_p * R + h % R;
+  }
+  if (a.S_max > 0) {
+    const int b = token / a.Tq, it = token % a.Tq, tt = it / a.box_s;
+    int at = a.starts[a.bins_p + b / a.bin_s], t0;
+    for (int i = b / a.bin_s * a.bin_s; i < b; ++i) at += a.Hkv * suffix_cost(a, suffix_seq(a, i));
+    const Seq s = suffix_seq(a, b);
+    at += hk * suffix_cost(a, s) + kUnitCost;
+    for (int i = 0; i < tt; ++i) at += unit_cost(unit_tiles(a, s, 1, i, &t0));
+    const int tiles = unit_tiles(a, s, 1, tt, &t0);
+    if (tiles > 0) {
+      first[1] = (b * a.Hkv + hk) * a.tiles_s + tt + at / share;
+      count[1] = (at + tiles - 1) / share - at / share + 1;
+    }
+    tr[1] = it % a.box_s * R + h % R;
+  }
+  const int parts = count[0] + count[1];
+  auto place = [&](int p, const float** lse, const float** o) {
+    const int side = p >= count[0];
+    const long long r = (first[side] + p - (side ? count[0] : 0)) * ((side ? a.box_s : a.box_p) * R) + tr[side];
+    *lse = (side ? a.part_ls : a.part_lp) + r;
+    *o = (side ? a.part_os : a.part_op) + r * kD;
+  };
   float m = -INFINITY;
-  for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_lse[p * rows + row]);
+  for (int p = lane; p < parts; p += 32) {
+    const float *l, *o;
+    place(p, &l, &o);
+    m = fmaxf(m, *l);
+  }
   m = warp_max(m);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
   if (m != -INFINITY) {
-    for (int p0 = 0; p0 < parts; p0 += 32) {
-      const float l = p0 + lane < parts ? a.part_lse[(p0 + lane) * rows + row] : -INFINITY;
-      const float wt = ex2((l - m) * 1.4426950408889634f);
-      unsigned live = __ballot_sync(0xffffffffu, l != -INFINITY);
-      while (live != 0u) {
-        const int i = __ffs((int)live) - 1;
-        live &= live - 1;
-        const float wi = __shfl_sync(0xffffffffu, wt, i);
-        const float4 o = *reinterpret_cast<const float4*>(a.part_o + ((p0 + i) * rows + row) * kD + 4 * lane);
-        acc.x += wi * o.x, acc.y += wi * o.y, acc.z += wi * o.z, acc.w += wi * o.w;
-        sum += wi;
-      }
+    for (int p = 0; p < parts; ++p) {
+      const float *lp, *op;
+      place(p, &lp, &op);
+      const float l = *lp;
+      if (l == -INFINITY) continue;
+      const float w = ex2((l - m) * 1.4426950408889634f);
+      const float4 o = *reinterpret_cast<const float4*>(op + 4 * lane);
+      acc.x += w * o.x, acc.y += w * o.y, acc.z += w * o.z, acc.w += w * o.w;
+      sum += w;
     }
     const float inv = 1.0f / sum;
     acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
@@ -461,10 +685,7 @@ __global__ void __launch_bounds__(128) k_prefix_combine(const PrefixAttnArgs a) 
   if (lane == 0 && a.out_lse != nullptr) a.out_lse[row] = m == -INFINITY ? m : m + logf(sum);
 }
 
-int ceil_div(long long a, long long b) {
-  const long long c = (a + b - 1) / b;
-  return c < 0x7fffffffLL ? (int)c : 0x7fffffff;
-}
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // q [tokens, H, 128] with row stride ldq: box of R heads x box_tok tokens x 64 columns
 bool q_map(CUtensorMap* m, const void* q, long long ldq, int tokens, int H, int R, int box_tok) {
@@ -484,44 +705,49 @@ bool kv_map(CUtensorMap* m, const void* p, long long ld, long long ls, int seqs,
 
 }  // namespace
 
-// How the work is cut, from the sizes alone (the lengths stay on the device).
-// Units of about `target` equal shares of all key tiles keep two CTAs on each
-// of 148 SMs busy for several rounds; a split is never shorter than min_tiles.
-bool prefix_attn_plan(PrefixAttnArgs* a) {
+// The sizes that do not depend on the lengths, and the workspace's bytes; false
+// where a count does not fit an int.
+bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes) {
   const int R = a->H / a->Hkv;
   a->rows_per_group = a->B / a->G;
+  a->ctas = kPrefixCtas;
   const int fit = kRows / R;  // tokens whose query rows fit a tile
-  const int tok_p = a->rows_per_group * a->Tq;
-  a->box_p = fit < tok_p ? fit : tok_p;
+  const long long tok_p = (long long)a->rows_per_group * a->Tq;
+  a->box_p = (int)(fit < tok_p ? fit : tok_p);
   a->box_s = fit < a->Tq ? fit : a->Tq;
-  a->tiles_p = ceil_div(tok_p, a->box_p);
-  a->tiles_s = ceil_div(a->Tq, a->box_s);
-  // rows of a group differ in position by at most S_max, so a window limits the prefix keys that any of them sees
-  const long long see_p = a->window < a->P_max ? (long long)a->window + a->S_max + a->Tq : a->P_max;
-  const int kt_p = ceil_div(see_p < a->P_max ? see_p : a->P_max, kKeys) + (a->window < a->P_max ? 1 : 0);
-  const long long see_s = (long long)a->window + a->Tq;
-  const int kt_s = ceil_div(see_s < a->S_max ? see_s : a->S_max, kKeys) + (see_s < a->S_max ? 1 : 0);
-  const long long base_p = a->P_max > 0 ? (long long)a->G * a->Hkv * a->tiles_p : 0;
-  const long long base_s = a->S_max > 0 ? (long long)a->B * a->Hkv * a->tiles_s : 0;
-  const long long work = base_p * kt_p + base_s * kt_s;
-  const int target = 4 * 296;
-  int chunk = ceil_div(work, target);
-  a->min_tiles = chunk < 2 ? 1 : 2;
-  if (chunk < 1) chunk = 1;
-  a->splits_p = base_p > 0 ? ceil_div(kt_p, chunk) : 0;
-  a->splits_s = base_s > 0 ? ceil_div(kt_s, chunk) : 0;
-  if (a->splits_p > kPrefixMaxSplits) a->splits_p = kPrefixMaxSplits;
-  if (a->splits_s > kPrefixMaxSplits) a->splits_s = kPrefixMaxSplits;
-  const long long up = base_p * a->splits_p, us = base_s * a->splits_s;
-  if (up + us > 0x7fffffffLL) return false;
-  a->units_p = (int)up;
-  a->units = (int)(up + us);
+  a->tiles_p = (int)ceil_div(tok_p, a->box_p);
+  a->tiles_s = (int)ceil_div(a->Tq, a->box_s);
+  a->bin_p = (int)ceil_div(a->G, kMaxBins);
+  a->bin_s = (int)ceil_div(a->B, kMaxBins);
+  a->bins_p = a->P_max > 0 ? (int)ceil_div(a->G, a->bin_p) : 0;
+  a->bins_s = a->S_max > 0 ? (int)ceil_div(a->B, a->bin_s) : 0;
+  const long long units_p = a->P_max > 0 ? (long long)a->G * a->Hkv * a->tiles_p : 0;
+  const long long units_s = a->S_max > 0 ? (long long)a->B * a->Hkv * a->tiles_s : 0;
+  // the cost of everything and its product with the CTAs' number fit an int
+  const long long most = 0x7fffffffLL / 2;
+  if (units_p > most || units_s > most) return false;
+  if (units_p * (ceil_div(a->P_max, kKeys) + kUnitCost) + units_s * (ceil_div(a->S_max, kKeys) + kUnitCost) > most) return false;
+  auto align = [](size_t b) { return (b + 255) & ~size_t(255); };
+  const size_t rows_p = units_p > 0 ? (size_t)(units_p + a->ctas) * (a->box_p * R) : 0;
+  const size_t rows_s = units_s > 0 ? (size_t)(units_s + a->ctas) * (a->box_s * R) : 0;
+  a->off_os = rows_p * kD * 4;
+  a->off_lp = a->off_os + rows_s * kD * 4;
+  a->off_ls = a->off_lp + align(rows_p * 4);
+  a->off_starts = a->off_ls + align(rows_s * 4);
+  *bytes = a->off_starts + align((2 * kMaxBins + 2) * 4);
   return true;
 }
 
-bool launch_prefix_attn(const PrefixAttnArgs& a, const void* q, long long ldq, const void* kp, const void* vp,
+bool launch_prefix_attn(const PrefixAttnArgs& args, const void* q, long long ldq, const void* kp, const void* vp,
                         long long ldp, long long lsp, const void* ks, const void* vs, long long lds, long long lss,
-                        cudaStream_t st) {
+                        void* workspace, cudaStream_t st) {
+  PrefixAttnArgs a = args;
+  char* ws = static_cast<char*>(workspace);
+  a.part_op = reinterpret_cast<float*>(ws);
+  a.part_os = reinterpret_cast<float*>(ws + a.off_os);
+  a.part_lp = reinterpret_cast<float*>(ws + a.off_lp);
+  a.part_ls = reinterpret_cast<float*>(ws + a.off_ls);
+  a.starts = reinterpret_cast<int*>(ws + a.off_starts);
   CUtensorMap m[6];
   const int tokens = a.B * a.Tq, R = a.H / a.Hkv;
   if (!q_map(&m[0], q, ldq, tokens, a.H, R, a.box_p) || !q_map(&m[1], q, ldq, tokens, a.H, R, a.box_s)) return false;
@@ -533,11 +759,10 @@ bool launch_prefix_attn(const PrefixAttnArgs& a, const void* q, long long ldq, c
   if (!smem_optin(k_prefix_attn, SMEM_BYTES)) return false;
   {
     LaunchScope scope_(KK_PREFIX_ATTN, st);
-    if (launch_pdl(k_prefix_attn, dim3(a.units), dim3(kThreads), SMEM_BYTES, st, 1, m[0], m[1], m[2], m[3], m[4], m[5], a) !=
+    if (launch_pdl(k_prefix_attn, dim3(a.ctas), dim3(kThreads), SMEM_BYTES, st, 1, m[0], m[1], m[2], m[3], m[4], m[5], a) !=
         cudaSuccess)
       return false;
   }
-  if (a.splits_p + a.splits_s == 1) return true;
   const long long rows = (long long)tokens * a.H;
   LaunchScope scope_(KK_PREFIX_ATTN, st);
   return launch_pdl(k_prefix_combine, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, a) == cudaSuccess;

@@ -932,26 +932,21 @@ int nc_qk_norm_rope_backward(const void* q, long long ldq, const void* k, long l
 
 // Sizes of a shared-prefix attention call and how its work is cut; false on
 // sizes the kernel does not take.
-static bool prefix_attn_sizes(PrefixAttnArgs* a, int B, int G, int Tq, int H, int Hkv, int P_max, int S_max, int window) {
+static bool prefix_attn_sizes(PrefixAttnArgs* a, size_t* bytes, int B, int G, int Tq, int H, int Hkv, int P_max, int S_max,
+                              int window) {
   memset(a, 0, sizeof(*a));
   if (B <= 0 || G <= 0 || B % G != 0 || Tq <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || H / Hkv > 128) return false;
   if (P_max < 0 || S_max < 0 || (long long)P_max + S_max == 0 || (long long)P_max + S_max > (1 << 30)) return false;
   if ((long long)B * Tq > 0x7fffffffLL / H) return false;
   a->B = B, a->G = G, a->Tq = Tq, a->H = H, a->Hkv = Hkv, a->P_max = P_max, a->S_max = S_max;
   a->window = (window <= 0 || window > P_max + S_max) ? P_max + S_max : window;
-  return prefix_attn_plan(a);
-}
-
-static size_t prefix_attn_bytes(const PrefixAttnArgs& a, size_t* lse_at) {
-  const size_t parts = (size_t)a.splits_p + a.splits_s, rows = (size_t)a.B * a.Tq * a.H;
-  *lse_at = parts * rows * 512;
-  return parts == 1 ? 0 : *lse_at + align256(parts * rows * 4);
+  return prefix_attn_plan(a, bytes);
 }
 
 size_t nc_prefix_attention_workspace_bytes(int B, int G, int Tq, int H, int Hkv, int P_max, int S_max, int window) {
   PrefixAttnArgs a;
-  size_t at;
-  return prefix_attn_sizes(&a, B, G, Tq, H, Hkv, P_max, S_max, window) ? prefix_attn_bytes(a, &at) : 0;
+  size_t bytes;
+  return prefix_attn_sizes(&a, &bytes, B, G, Tq, H, Hkv, P_max, S_max, window) ? bytes : 0;
 }
 
 int nc_prefix_attention(const void* q, long long ldq, const void* k_prefix, const void* v_prefix, long long ldp,
@@ -964,7 +959,8 @@ int nc_prefix_attention(const void* q, long long ldq, const void* k_prefix, cons
   if (P_max > 0 && (!k_prefix || !v_prefix || !prefix_lens)) return NC_ERR_ARG;
   if (S_max > 0 && (!k_suffix || !v_suffix || !suffix_lens)) return NC_ERR_ARG;
   PrefixAttnArgs a;
-  if (D != 128 || !prefix_attn_sizes(&a, B, G, Tq, H, Hkv, P_max, S_max, window)) return NC_ERR_SHAPE;
+  size_t need;
+  if (D != 128 || !prefix_attn_sizes(&a, &need, B, G, Tq, H, Hkv, P_max, S_max, window)) return NC_ERR_SHAPE;
   const long long kv = (long long)Hkv * D, far = 1LL << 38;  // strides in bytes stay below 2^40
   if (ldq < (long long)H * D || ldq > far / ((long long)B * Tq)) return NC_ERR_SHAPE;
   if (P_max > 0 && (ldp < kv || ldp > far / P_max || (G > 1 && (lsp < ldp * (P_max - 1) + kv || lsp > far)))) return NC_ERR_SHAPE;
@@ -974,9 +970,7 @@ int nc_prefix_attention(const void* q, long long ldq, const void* k_prefix, cons
     return NC_ERR_ALIGN;
   if (P_max > 0 && (!aligned16(k_prefix) || !aligned16(v_prefix) || ldp % 8 != 0 || (G > 1 && lsp % 8 != 0))) return NC_ERR_ALIGN;
   if (S_max > 0 && (!aligned16(k_suffix) || !aligned16(v_suffix) || lds % 8 != 0 || (B > 1 && lss % 8 != 0))) return NC_ERR_ALIGN;
-  size_t lse_at;
-  const size_t need = prefix_attn_bytes(a, &lse_at);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return NC_ERR_WORKSPACE;
+  if (workspace == nullptr || workspace_bytes < need) return NC_ERR_WORKSPACE;
   DevInfo d;
   if (!dev_info(&d)) return NC_ERR_CUDA;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -984,10 +978,8 @@ int nc_prefix_attention(const void* q, long long ldq, const void* k_prefix, cons
   a.suffix_lens = S_max > 0 ? suffix_lens : nullptr;
   a.out = static_cast<bf16*>(out);
   a.out_lse = out_lse_opt;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_lse = need > 0 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + lse_at) : nullptr;
   a.status = d.status;
-  if (!launch_prefix_attn(a, q, ldq, k_prefix, v_prefix, ldp, lsp, k_suffix, v_suffix, lds, lss,
+  if (!launch_prefix_attn(a, q, ldq, k_prefix, v_prefix, ldp, lsp, k_suffix, v_suffix, lds, lss, workspace,
                           static_cast<cudaStream_t>(stream))) {
     check_launch("nc_prefix_attention");
     return NC_ERR_CUDA;

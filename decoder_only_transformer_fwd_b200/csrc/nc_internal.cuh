@@ -226,23 +226,27 @@ void launch_qk_norm_rope(const QkNormArgs& p, int act_bf16, cudaStream_t st);
 void launch_qk_norm_rope_bwd(const QkNormArgs& p, int act_bf16, cudaStream_t st);
 
 // Attention over a shared prefix and the rows' own keys (k_prefix_attn.cu).
-constexpr int kPrefixMaxSplits = 128;
+constexpr int kPrefixCtas = 296;  // two on each of 148 SMs
 struct PrefixAttnArgs {
   int B, G, Tq, H, Hkv, P_max, S_max, window;
   float scale_log2;  // softmax_scale * log2(e)
   const int32_t *prefix_lens, *suffix_lens;
   bf16* out;
   float* out_lse;
-  float *part_o, *part_lse;  // workspace: [parts, B Tq H, 128] and [parts, B Tq H]
   int* status;
-  // filled by prefix_attn_plan()
-  int rows_per_group, box_p, box_s, tiles_p, tiles_s, splits_p, splits_s, min_tiles, units_p, units;
+  // filled by prefix_attn_plan(): query tokens per tile and tiles per sequence
+  // (prefix, suffix), sequences per bin and bins of the tables of starts
+  int rows_per_group, ctas, box_p, box_s, tiles_p, tiles_s, bin_p, bin_s, bins_p, bins_s;
+  size_t off_os, off_lp, off_ls, off_starts;
+  // workspace: pieces' outputs and log-sum-exps, prefix and suffix; the tables
+  float *part_op, *part_os, *part_lp, *part_ls;
+  int* starts;
 };
-// false where the units do not fit an int
-bool prefix_attn_plan(PrefixAttnArgs* a);
+// false where a count does not fit an int
+bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes);
 bool launch_prefix_attn(const PrefixAttnArgs& a, const void* q, long long ldq, const void* kp, const void* vp,
                         long long ldp, long long lsp, const void* ks, const void* vs, long long lds, long long lss,
-                        cudaStream_t st);
+                        void* workspace, cudaStream_t st);
 
 // Clipped policy loss (k_policy.cu); part: 3 doubles per CTA.
 constexpr int kPolicyMaxCtas = 1024;

@@ -8,6 +8,7 @@ build raises immediately; there is no fallback path.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -340,31 +341,23 @@ def nc_prefix_ce(x, w_u, targets, out_loss, vocab: int, widths, eps: float = 1e-
                               cap, _ptr(workspace), nbytes, _stream(stream)), "nc_prefix_ce")
 
 
-def _operands(what: str, *items):
-    """Checks tensors before their pointers are handed over.  items: (name,
-    tensor or None, shape with None for any size, dtype).  All tensors must be
-    on the current CUDA device: the call runs there, on one of its streams."""
+def _mismatch(what: str, name: str, t, shape, dtype):
+    """Raises for a tensor that is not what the call takes.  All tensors must
+    be on the current CUDA device: the call runs there, on one of its streams."""
     import torch
-    dev = None
-    for name, t, shape, dtype in items:
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise NcError(f"{what}: {name} is {t.dtype}, expected {dtype}")
-        if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-            raise NcError(f"{what}: {name} has shape {tuple(t.shape)}, expected {shape}")
-        if not t.is_cuda:
-            raise NcError(f"{what}: {name} is not on a CUDA device")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise NcError(f"{what}: {name} is on {t.device}, the current device is cuda:{dev}")
+    if t is None:
+        raise NcError(f"{what}: {name} is missing")
+    if t.dtype != dtype:
+        raise NcError(f"{what}: {name} is {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise NcError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise NcError(f"{what}: {name} is not on a CUDA device")
+    raise NcError(f"{what}: {name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _packed(what: str, name: str, t, first: int = 0):
     """t's dimensions from `first` on are laid out without gaps."""
-    if t is None or t.is_contiguous() and first == 0:
-        return
     want = 1
     for n, s in zip(reversed(t.shape[first:]), reversed(t.stride()[first:])):
         if n > 1 and s != want:
@@ -380,21 +373,51 @@ def _act_dtype(what: str, t):
     return NC_BF16 if t.dtype == torch.bfloat16 else NC_FP32
 
 
-def _row(t):
-    """Row stride of t [rows, ...]; a single row has any."""
-    return 0 if t is None else (t.stride(0) if t.shape[0] > 1 else t[0].numel())
+def _take(what: str, name: str, t, shape, dtype, dev: int, packed: int = 0):
+    """Address of t, whose dimensions from `packed` (0 or the last two) on have
+    no gaps.  Runs on every call, next to kernels of a few microseconds: what a
+    correct call needs is compared here, the rest is left to _mismatch and
+    _packed."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _mismatch(what, name, t, shape, dtype)
+    if packed == 0:
+        if not t.is_contiguous():
+            _packed(what, name, t)
+    else:
+        st = t.stride()
+        if st[-1] != 1 or (packed == len(shape) - 2 and st[-2] != shape[-1]):
+            _packed(what, name, t, packed)
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _scratch(workspace, nbytes: int, like):
-    """(workspace, its bytes): the caller's, or a new one of nbytes."""
+    """(workspace, its address, its bytes): the caller's, or a new one of nbytes."""
     import torch
-    if workspace is None and nbytes > 0:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     if workspace is None:
-        return None, 0
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return workspace, workspace.data_ptr(), nbytes
     if workspace.device != like.device or not workspace.is_contiguous():
         raise NcError("workspace: a contiguous tensor on the operands' device is needed")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _heads_of(what: str, name: str, t):
+    if t.dim() != 3:
+        raise NcError(f"{what}: {name} is [N, heads, D]")
+    return t.shape
+
+
+def _rows_of(what: str, name: str, t, shape, dtype, dev: int):
+    """(address, row stride) of t [rows, heads, D]; a single row has any stride."""
+    p = _take(what, name, t, shape, dtype, dev, 1)
+    return p, t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
 
 
 def nc_qk_norm_rope(q, k, positions, q_out, k_out, v=None, v_out=None, slots=None, alpha: float = 1.15,
@@ -403,27 +426,28 @@ def nc_qk_norm_rope(q, k, positions, q_out, k_out, v=None, v_out=None, slots=Non
     go to rows slots [N] (int32, -1 = not kept) of k_out and v_out [rows, H_kv, D], or to rows 0..N-1."""
     import torch
     what = "nc_qk_norm_rope"
-    dt = _act_dtype(what, q)
-    if q.dim() != 3 or k.dim() != 3:
-        raise NcError(f"{what}: q and k are [N, heads, D]")
-    N, H, D = q.shape
-    Hkv, rows = k.shape[1], k_out.shape[0]
+    dt, ty, dev = _act_dtype(what, q), q.dtype, torch.cuda.current_device() if q.is_cuda else None
+    N, H, D = _heads_of(what, "q", q)
+    Hkv, rows = _heads_of(what, "k", k)[1], _heads_of(what, "k_out", k_out)[0]
     if (v is None) != (v_out is None):
         raise NcError(f"{what}: v and v_out come together")
-    _operands(what, ("q", q, (N, H, D), q.dtype), ("k", k, (N, Hkv, D), q.dtype), ("v", v, (N, Hkv, D), q.dtype),
-              ("positions", positions, (N,), torch.int32), ("slots", slots, (N,), torch.int32),
-              ("q_out", q_out, (N, H, D), q.dtype), ("k_out", k_out, (rows, Hkv, D), q.dtype),
-              ("v_out", v_out, (rows, Hkv, D), q.dtype))
-    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out), ("v_out", v_out)):
-        _packed(what, name, t, 1)
-    _packed(what, "positions", positions)
-    _packed(what, "slots", slots)
+    pq, ldq = _rows_of(what, "q", q, (N, H, D), ty, dev)
+    pk, ldk = _rows_of(what, "k", k, (N, Hkv, D), ty, dev)
+    po, ldo = _rows_of(what, "q_out", q_out, (N, H, D), ty, dev)
+    pc, ldc = _rows_of(what, "k_out", k_out, (rows, Hkv, D), ty, dev)
+    pv = pd = None
+    ldv = ldd = 0
+    if v is not None:
+        pv, ldv = _rows_of(what, "v", v, (N, Hkv, D), ty, dev)
+        pd, ldd = _rows_of(what, "v_out", v_out, (rows, Hkv, D), ty, dev)
+    pp = _take(what, "positions", positions, (N,), torch.int32, dev)
+    ps = None if slots is None else _take(what, "slots", slots, (N,), torch.int32, dev)
     if N == 0:
         return
-    _check(lib().nc_qk_norm_rope(_ptr(q), _row(q), _ptr(k), _row(k), _ptr(v), _row(v), _ptr(positions), _ptr(slots),
-                                 N, H, Hkv, D, _ptr(q_out), _row(q_out), _ptr(k_out), _row(k_out) if rows else Hkv * D,
-                                 _ptr(v_out), (_row(v_out) if rows else Hkv * D) if v_out is not None else 0, rows,
-                                 alpha, rope_base, eps, dt, _stream(stream)), what)
+    rc = lib().nc_qk_norm_rope(pq, ldq, pk, ldk, pv, ldv, pp, ps, N, H, Hkv, D, po, ldo, pc, ldc, pd, ldd, rows,
+                               alpha, rope_base, eps, dt, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, what)
 
 
 def nc_qk_norm_rope_backward(q, k, positions, dq_hat, dk_hat, out_dq, out_dk, alpha: float = 1.15,
@@ -431,27 +455,66 @@ def nc_qk_norm_rope_backward(q, k, positions, dq_hat, dk_hat, out_dq, out_dk, al
     """Gradients of q [N, H, D] and k [N, H_kv, D] from those of nc_qk_norm_rope's qhat and khat."""
     import torch
     what = "nc_qk_norm_rope_backward"
-    dt = _act_dtype(what, q)
-    if q.dim() != 3 or k.dim() != 3:
-        raise NcError(f"{what}: q and k are [N, heads, D]")
-    N, H, D = q.shape
-    Hkv = k.shape[1]
-    _operands(what, ("q", q, (N, H, D), q.dtype), ("k", k, (N, Hkv, D), q.dtype),
-              ("positions", positions, (N,), torch.int32), ("dq_hat", dq_hat, (N, H, D), q.dtype),
-              ("dk_hat", dk_hat, (N, Hkv, D), q.dtype), ("out_dq", out_dq, (N, H, D), q.dtype),
-              ("out_dk", out_dk, (N, Hkv, D), q.dtype))
-    for name, t in (("q", q), ("k", k), ("dq_hat", dq_hat), ("dk_hat", dk_hat), ("out_dq", out_dq), ("out_dk", out_dk)):
-        _packed(what, name, t, 1)
-    _packed(what, "positions", positions)
+    dt, ty, dev = _act_dtype(what, q), q.dtype, torch.cuda.current_device() if q.is_cuda else None
+    N, H, D = _heads_of(what, "q", q)
+    Hkv = _heads_of(what, "k", k)[1]
+    pq, ldq = _rows_of(what, "q", q, (N, H, D), ty, dev)
+    pk, ldk = _rows_of(what, "k", k, (N, Hkv, D), ty, dev)
+    pg, ldg = _rows_of(what, "dq_hat", dq_hat, (N, H, D), ty, dev)
+    ph, ldh = _rows_of(what, "dk_hat", dk_hat, (N, Hkv, D), ty, dev)
+    pd, ldd = _rows_of(what, "out_dq", out_dq, (N, H, D), ty, dev)
+    pe, lde = _rows_of(what, "out_dk", out_dk, (N, Hkv, D), ty, dev)
+    pp = _take(what, "positions", positions, (N,), torch.int32, dev)
     if N == 0:
         return
-    _check(lib().nc_qk_norm_rope_backward(_ptr(q), _row(q), _ptr(k), _row(k), _ptr(positions), _ptr(dq_hat), _row(dq_hat),
-                                          _ptr(dk_hat), _row(dk_hat), N, H, Hkv, D, _ptr(out_dq), _row(out_dq),
-                                          _ptr(out_dk), _row(out_dk), alpha, rope_base, eps, dt, _stream(stream)), what)
+    rc = lib().nc_qk_norm_rope_backward(pq, ldq, pk, ldk, pp, pg, ldg, ph, ldh, N, H, Hkv, D, pd, ldd, pe, lde, alpha,
+                                        rope_base, eps, dt, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, what)
 
 
 def nc_prefix_attention_workspace_bytes(B, G, Tq, H, Hkv, P_max, S_max, window: int = 0) -> int:
     return int(lib().nc_prefix_attention_workspace_bytes(B, G, Tq, H, Hkv, P_max, S_max, window))
+
+
+@functools.lru_cache(maxsize=256)
+def _prefix_attention_bytes(*sizes) -> int:
+    return nc_prefix_attention_workspace_bytes(*sizes)
+
+
+def _cache_of(what: str, side: str, k, v, lens, n, D: int, dev: int):
+    """One side's caches [sequences, keys, H_kv, D]: (k, v, strides, lens, sequences, keys, H_kv)."""
+    import torch
+    if k is None:
+        if v is not None or lens is not None:
+            raise NcError(f"{what}: k, v and lengths of the {side} come together")
+        return None, None, 0, 0, None, 1, 0, None
+    if v is None or lens is None:
+        raise NcError(f"{what}: k, v and lengths of the {side} come together")
+    if k.dim() != 4:
+        raise NcError(f"{what}: k_{side} is [sequences, keys, H_kv, D]")
+    seqs, cap, Hkv, Dk = shape = tuple(k.shape)
+    if Dk != D or (n is not None and seqs != n):
+        raise NcError(f"{what}: k_{side} has shape {shape}, expected ({n or 'G'}, keys, H_kv, {D})")
+    pk = _take(what, f"k_{side}", k, shape, torch.bfloat16, dev, 2)
+    pv = _take(what, f"v_{side}", v, shape, torch.bfloat16, dev, 2)
+    pl = _take(what, f"{side}_lens", lens, (seqs,), torch.int32, dev)
+    sk, sv = k.stride(), v.stride()
+    if (cap > 1 and sk[1] != sv[1]) or (seqs > 1 and sk[0] != sv[0]):
+        raise NcError(f"{what}: k_{side} and v_{side} must have the same strides")
+    if cap == 0:
+        return None, None, 0, 0, None, seqs, 0, Hkv
+    ld = sk[1] if cap > 1 else Hkv * D
+    return pk, pv, ld, sk[0] if seqs > 1 else ld * cap, pl, seqs, cap, Hkv
+
+
+def _even_rows(what: str, name: str, t, outer: int, inner: int, width: int) -> int:
+    """Stride between consecutive rows of t [outer, inner, ...], which must be evenly spaced."""
+    st = t.stride()
+    ld = st[1] if inner > 1 else (st[0] if outer > 1 else width)
+    if outer > 1 and inner > 1 and st[0] != inner * ld:
+        raise NcError(f"{what}: {name}'s rows must be evenly spaced (strides {st})")
+    return ld
 
 
 def nc_prefix_attention(q, k_prefix, v_prefix, prefix_lens, k_suffix, v_suffix, suffix_lens, out, out_lse=None,
@@ -461,50 +524,25 @@ def nc_prefix_attention(q, k_prefix, v_prefix, prefix_lens, k_suffix, v_suffix, 
     (suffix_lens [B] int32); one side may be None.  out [B, Tq, H, D], out_lse [B, Tq, H] fp32."""
     import torch
     what = "nc_prefix_attention"
-    bf, i32 = torch.bfloat16, torch.int32
+    dev = torch.cuda.current_device() if q.is_cuda else None
     if q.dim() != 4:
         raise NcError(f"{what}: q is [B, Tq, H, D]")
-    B, Tq, H, D = q.shape
-    sides = []
-    for side, k, v, lens, n in (("prefix", k_prefix, v_prefix, prefix_lens, None), ("suffix", k_suffix, v_suffix, suffix_lens, B)):
-        if (k is None) != (v is None) or (k is None) != (lens is None):
-            raise NcError(f"{what}: k, v and lengths of the {side} come together")
-        if k is None:
-            sides.append((None, None, 0, 0, None, 1, 0))
-            continue
-        if k.dim() != 4:
-            raise NcError(f"{what}: k_{side} is [sequences, keys, H_kv, D]")
-        seqs, cap, Hkv = k.shape[0], k.shape[1], k.shape[2]
-        _operands(what, (f"k_{side}", k, (n, None, None, D), bf), (f"v_{side}", v, tuple(k.shape), bf),
-                  (f"{side}_lens", lens, (seqs,), i32))
-        _packed(what, f"k_{side}", k, 2)
-        _packed(what, f"v_{side}", v, 2)
-        _packed(what, f"{side}_lens", lens)
-        ld = k.stride(1) if cap > 1 else Hkv * D
-        ls = k.stride(0) if seqs > 1 else ld * max(cap, 1)
-        if (cap > 1 and v.stride(1) != ld) or (seqs > 1 and v.stride(0) != ls):
-            raise NcError(f"{what}: k_{side} and v_{side} must have the same strides")
-        if cap == 0:
-            sides.append((None, None, 0, 0, None, seqs, 0))
-        else:
-            sides.append((k, v, ld, ls, lens, seqs, cap))
-    (kp, vp, ldp, lsp, pl, G, P), (ks, vs, lds, lss, sl, _, S) = sides
-    heads = {t.shape[2] for t in (k_prefix, k_suffix) if t is not None}
-    if len(heads) != 1:
-        raise NcError(f"{what}: " + ("there are no keys" if not heads else "prefix and suffix differ in key heads"))
-    Hkv = heads.pop()
-    _operands(what, ("q", q, (B, Tq, H, D), bf), ("out", out, (B, Tq, H, D), bf), ("out_lse", out_lse, (B, Tq, H), torch.float32))
-    _packed(what, "out", out)
-    _packed(what, "out_lse", out_lse)
-    _packed(what, "q", q, 2)
-    ldq = q.stride(1) if Tq > 1 else (q.stride(0) if B > 1 else H * D)
-    if B > 1 and Tq > 1 and q.stride(0) != Tq * ldq:
-        raise NcError(f"{what}: q's tokens must be evenly spaced (strides {tuple(q.stride())})")
+    B, Tq, H, D = shape = tuple(q.shape)
+    pq = _take(what, "q", q, shape, torch.bfloat16, dev, 2)
+    kp, vp, ldp, lsp, pl, G, P, hp = _cache_of(what, "prefix", k_prefix, v_prefix, prefix_lens, None, D, dev)
+    ks, vs, lds, lss, sl, _, S, hs = _cache_of(what, "suffix", k_suffix, v_suffix, suffix_lens, B, D, dev)
+    Hkv = hp if hs is None else hs
+    if Hkv is None or (hp is not None and hp != Hkv):
+        raise NcError(f"{what}: " + ("there are no keys" if Hkv is None else "prefix and suffix differ in key heads"))
+    po = _take(what, "out", out, shape, torch.bfloat16, dev)
+    pe = None if out_lse is None else _take(what, "out_lse", out_lse, (B, Tq, H), torch.float32, dev)
+    ldq = _even_rows(what, "q", q, B, Tq, H * D)
     scale = D ** -0.5 if softmax_scale is None else softmax_scale
-    workspace, nbytes = _scratch(workspace, nc_prefix_attention_workspace_bytes(B, G, Tq, H, Hkv, P, S, window), q)
-    _check(lib().nc_prefix_attention(_ptr(q), ldq, _ptr(kp), _ptr(vp), ldp, lsp, _ptr(pl), _ptr(ks), _ptr(vs), lds, lss,
-                                     _ptr(sl), _ptr(out), _ptr(out_lse), B, G, Tq, H, Hkv, D, P, S, window, scale,
-                                     _ptr(workspace), nbytes, _stream(stream)), what)
+    workspace, pw, nbytes = _scratch(workspace, _prefix_attention_bytes(B, G, Tq, H, Hkv, P, S, window), q)
+    rc = lib().nc_prefix_attention(pq, ldq, kp, vp, ldp, lsp, pl, ks, vs, lds, lss, sl, po, pe, B, G, Tq, H, Hkv, D,
+                                   P, S, window, scale, pw, nbytes, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, what)
 
 
 def nc_policy_loss(logits, targets, advantages, out_stats, out_logp, out_dlogits=None, old_logp=None, ref_logp=None,
@@ -514,33 +552,33 @@ def nc_policy_loss(logits, targets, advantages, out_stats, out_logp, out_dlogits
     [B] or [B, T]: out_stats [3] (loss, mean KL, clipped share), out_logp [B, T], out_dlogits [B, T, V]."""
     import torch
     what = "nc_policy_loss"
-    dt = _act_dtype(what, logits)
-    f32 = torch.float32
+    dt, ty, f32 = _act_dtype(what, logits), logits.dtype, torch.float32
+    dev = torch.cuda.current_device() if logits.is_cuda else None
     if logits.dim() != 3:
         raise NcError(f"{what}: logits are [B, T, V]")
-    B, T, V = logits.shape
-    per_token = advantages.dim() == 2
-    _operands(what, ("logits", logits, (B, T, V), logits.dtype), ("targets", targets, (B, T), torch.int32),
-              ("advantages", advantages, (B, T) if per_token else (B,), f32), ("old_logp", old_logp, (B, T), f32),
-              ("ref_logp", ref_logp, (B, T), f32), ("out_stats", out_stats, (3,), f32), ("out_logp", out_logp, (B, T), f32),
-              ("out_dlogits", out_dlogits, (B, T, V), logits.dtype))
-    for name, t in (("targets", targets), ("advantages", advantages), ("old_logp", old_logp), ("ref_logp", ref_logp),
-                    ("out_stats", out_stats), ("out_logp", out_logp)):
-        _packed(what, name, t)
+    B, T, V = shape = tuple(logits.shape)
+    bt, per_token = (B, T), advantages.dim() == 2
+    pz = _take(what, "logits", logits, shape, ty, dev, 2)
+    py = _take(what, "targets", targets, bt, torch.int32, dev)
+    pa = _take(what, "advantages", advantages, bt if per_token else (B,), f32, dev)
+    ps = _take(what, "out_stats", out_stats, (3,), f32, dev)
+    pl = _take(what, "out_logp", out_logp, bt, f32, dev)
+    po = None if old_logp is None else _take(what, "old_logp", old_logp, bt, f32, dev)
+    pr = None if ref_logp is None else _take(what, "ref_logp", ref_logp, bt, f32, dev)
+    ldl, pd, lddl = _even_rows(what, "logits", logits, B, T, V), None, 0
+    if out_dlogits is not None:
+        pd = _take(what, "out_dlogits", out_dlogits, shape, ty, dev, 2)
+        lddl = _even_rows(what, "out_dlogits", out_dlogits, B, T, V)
+    workspace, pw, nbytes = _scratch(workspace, _policy_bytes(), logits)
+    rc = lib().nc_policy_loss(pz, ldl, py, pa, per_token, po, pr, B, T, V, clip_low, clip_high, kl_beta, norm, ps, pl, pd, lddl,
+                              dt, pw, nbytes, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, what)
 
-    def row_stride(name, t):
-        _packed(what, name, t, 2)
-        ld = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else V)
-        if B > 1 and T > 1 and t.stride(0) != T * ld:
-            raise NcError(f"{what}: {name}'s rows must be evenly spaced (strides {tuple(t.stride())})")
-        return ld
 
-    ldl = row_stride("logits", logits)
-    lddl = row_stride("out_dlogits", out_dlogits) if out_dlogits is not None else 0
-    workspace, nbytes = _scratch(workspace, int(lib().nc_policy_loss_workspace_bytes()), logits)
-    _check(lib().nc_policy_loss(_ptr(logits), ldl, _ptr(targets), _ptr(advantages), int(per_token), _ptr(old_logp),
-                                _ptr(ref_logp), B, T, V, clip_low, clip_high, kl_beta, norm, _ptr(out_stats), _ptr(out_logp),
-                                _ptr(out_dlogits), lddl, dt, _ptr(workspace), nbytes, _stream(stream)), what)
+@functools.lru_cache(maxsize=1)
+def _policy_bytes() -> int:
+    return int(lib().nc_policy_loss_workspace_bytes())
 
 
 def nc_get_status(stream=None) -> tuple[int, int]:

@@ -81,10 +81,10 @@ def test_prefix_attention_refuses(kw, status):
 
 def test_prefix_attention_workspace():
     need = nc.nc_prefix_attention_workspace_bytes
-    # every part holds 512 + 4 bytes per query row
+    # either side holds 512 + 4 bytes per query row at least
     assert need(4, 2, 1, 4, 2, 10, 5, 0) >= 2 * 4 * 4 * 516
+    assert need(4, 2, 1, 4, 2, 10, 0, 0) < need(4, 2, 1, 4, 2, 10, 5, 0)
     assert need(4, 3, 1, 4, 2, 10, 5, 0) == 0 and need(4, 2, 1, 4, 3, 10, 5, 0) == 0
-    assert need(1, 1, 1, 1, 1, 64, 0, 0) == 0          # one part in all: the output is written at once
     assert _call("nc_prefix_attention", PA_NAMES, PA_BASE, wsb=need(4, 2, 1, 4, 2, 10, 5, 0) - 1) == S["NC_ERR_WORKSPACE"]
 
 
