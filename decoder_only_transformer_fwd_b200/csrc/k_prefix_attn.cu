@@ -53,7 +53,8 @@ constexpr int OFF_SLOT = 2 * Q_BOX;
 constexpr int OFF_BAR = OFF_SLOT + SLOTS * SLOT_BYTES;
 constexpr int OFF_PIECE = OFF_BAR + 256;
 constexpr int OFF_START = OFF_PIECE + kPieces * 64;
-constexpr int SMEM_BYTES = OFF_START + (2 * kMaxBins + 2) * 4 + 1024;
+constexpr int OFF_SEEN = OFF_START + (2 * kMaxBins + 2) * 4;
+constexpr int SMEM_BYTES = OFF_SEEN + kMaxBins * 8 + 1024;
 static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
 constexpr int kThreads = 192, kWarpTma = 4, kWarpMma = 5;
 constexpr uint32_t TMEM_COLS = 256;        // S0 64 | S1 64 | O 128
@@ -78,22 +79,27 @@ struct Seq {  // a group's prefix or a row's own keys
 
 __device__ __forceinline__ int clamp_len(int n, int most) { return min(max(n, 0), most); }
 
-// Keys [lo, hi) of group g's prefix that a query of one of its rows sees.  All
-// lanes of the warp together: a window makes lo depend on the shortest row.
-__device__ __forceinline__ Seq prefix_seq(const PrefixAttnArgs& a, int g, int lane) {
+// shortest own length of a group's rows from r0 on, every `step`-th
+__device__ __forceinline__ int least_suffix(const PrefixAttnArgs& a, int g, int r0, int step) {
+  if (a.S_max == 0) return 0;
+  int least = a.S_max;
+  for (int r = r0; r < a.rows_per_group; r += step)
+    least = min(least, clamp_len(a.suffix_lens[g * a.rows_per_group + r], a.S_max));
+  return least;
+}
+
+// Keys [lo, hi) of group g's prefix that a query of one of its rows sees; a
+// window makes lo depend on the shortest row.
+__device__ __forceinline__ Seq prefix_seq(const PrefixAttnArgs& a, int g, int least) {
   Seq s;
   s.P = s.hi = clamp_len(a.prefix_lens[g], a.P_max);
-  s.S = s.lo = 0;
-  if (a.window < a.P_max + a.S_max) {
-    int least = a.S_max;
-    if (a.S_max > 0) {
-      for (int r = lane; r < a.rows_per_group; r += 32)
-        least = min(least, clamp_len(a.suffix_lens[g * a.rows_per_group + r], a.S_max));
-      least = __reduce_min_sync(0xffffffffu, least);
-    }
-    s.lo = min(s.P, max(0, s.P + least - a.Tq - a.window + 1));
-  }
+  s.S = 0;
+  s.lo = min(s.P, max(0, s.P + least - a.Tq - a.window + 1));
   return s;
+}
+__device__ __forceinline__ bool windowed(const PrefixAttnArgs& a) { return a.window < a.P_max + a.S_max; }
+__device__ __forceinline__ Seq prefix_seq(const PrefixAttnArgs& a, int g) {
+  return prefix_seq(a, g, windowed(a) ? least_suffix(a, g, 0, 1) : 0);
 }
 
 __device__ __forceinline__ Seq suffix_seq(const PrefixAttnArgs& a, int b) {
@@ -127,13 +133,18 @@ __device__ __forceinline__ int suffix_cost(const PrefixAttnArgs& a, const Seq& s
   return c;
 }
 
-// Fills the tables of starts (cost before each bin of groups, then of rows;
-// the last entry is the total).  All threads of the CTA.
-__device__ void fill_starts(const PrefixAttnArgs& a, int* start, int warp, int lane) {
+// Fills the tables: start[i], the cost before each bin of groups, then of rows
+// (the last entry is the total), and lo[g], hi[g] of each group's prefix where a
+// bin is one group.  All threads of the CTA.
+__device__ void fill_tables(const PrefixAttnArgs& a, int* start, int2* seen, int warp, int lane) {
   for (int i = warp; i < a.bins_p; i += kThreads / 32) {
     int c = 0, t0;
-    for (int g = i * a.bin_p; g < min(a.G, (i + 1) * a.bin_p); ++g)
-      c += a.Hkv * a.tiles_p * unit_cost(unit_tiles(a, prefix_seq(a, g, lane), 0, 0, &t0));
+    for (int g = i * a.bin_p; g < min(a.G, (i + 1) * a.bin_p); ++g) {
+      const int least = windowed(a) ? __reduce_min_sync(0xffffffffu, least_suffix(a, g, lane, 32)) : 0;
+      const Seq s = prefix_seq(a, g, least);
+      c += a.Hkv * a.tiles_p * unit_cost(unit_tiles(a, s, 0, 0, &t0));
+      if (lane == 0 && a.bin_p == 1) seen[g] = make_int2(s.lo, s.hi);
+    }
     if (lane == 0) start[i] = c;
   }
   for (int i = threadIdx.x; i < a.bins_s; i += kThreads) {
@@ -164,6 +175,15 @@ __device__ void fill_starts(const PrefixAttnArgs& a, int* start, int warp, int l
   __syncthreads();
 }
 
+__device__ __forceinline__ Seq group_seq(const PrefixAttnArgs& a, const int2* seen, int g) {
+  if (a.bin_p > 1) return prefix_seq(a, g);
+  Seq s;
+  s.P = s.hi = seen[g].y;
+  s.S = 0;
+  s.lo = seen[g].x;
+  return s;
+}
+
 // share of the total cost that a CTA takes
 __device__ __forceinline__ int share_of(const PrefixAttnArgs& a, int total) {
   return max((total + a.ctas - 1) / a.ctas, kUnitCost + 1);
@@ -171,9 +191,9 @@ __device__ __forceinline__ int share_of(const PrefixAttnArgs& a, int total) {
 
 // The piece that holds cost position v, as far as `end`; *next: the position
 // behind it.  A piece may have no tile (it holds only a unit's fixed cost).
-// All lanes of a warp together.  Lengths that change while the kernel runs give
-// wrong pieces, but every loop ends and every index stays in range.
-__device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, int v, int end, int lane, int* next) {
+// Lengths that change while the kernel runs give wrong pieces, but every loop
+// ends and every index stays in range.
+__device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, const int2* seen, int v, int end, int* next) {
   int lo = 0, hi = a.bins_p + a.bins_s;  // the last bin that starts at or before v
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -185,7 +205,7 @@ __device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, int v, int 
   Seq s;
   if (!p.suffix) {
     for (p.seq = lo * a.bin_p;; ++p.seq) {
-      s = prefix_seq(a, p.seq, lane);
+      s = group_seq(a, seen, p.seq);
       tiles = unit_tiles(a, s, 0, 0, &t0);
       const int all = a.Hkv * a.tiles_p * unit_cost(tiles);
       if (at < all || p.seq + 1 >= a.G) break;
@@ -225,6 +245,27 @@ __device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, int v, int 
   return p;
 }
 
+// Where the pieces of unit u of a side lie, for k_prefix_combine: (first slot,
+// count) = (u + first CTA, CTAs that hold one of its tiles).
+__device__ int2 unit_pieces(const PrefixAttnArgs& a, const int* start, const int2* seen, int share, int suffix, int u) {
+  const int tiles_q = suffix ? a.tiles_s : a.tiles_p, bin = suffix ? a.bin_s : a.bin_p;
+  const int tt = u % tiles_q, hk = u / tiles_q % a.Hkv, seq = u / tiles_q / a.Hkv, i0 = seq / bin * bin;
+  int at = start[(suffix ? a.bins_p : 0) + seq / bin] + kUnitCost, t0, tiles;
+  if (!suffix) {
+    for (int i = i0; i < seq; ++i) at += a.Hkv * a.tiles_p * unit_cost(unit_tiles(a, group_seq(a, seen, i), 0, 0, &t0));
+    tiles = unit_tiles(a, group_seq(a, seen, seq), 0, 0, &t0);
+    at += (hk * a.tiles_p + tt) * unit_cost(tiles);
+  } else {
+    for (int i = i0; i < seq; ++i) at += a.Hkv * suffix_cost(a, suffix_seq(a, i));
+    const Seq s = suffix_seq(a, seq);
+    at += hk * suffix_cost(a, s);
+    for (int i = 0; i < tt; ++i) at += unit_cost(unit_tiles(a, s, 1, i, &t0));
+    tiles = unit_tiles(a, s, 1, tt, &t0);
+  }
+  if (tiles == 0) return make_int2(0, 0);
+  return make_int2(u + at / share, (at + tiles - 1) / share - at / share + 1);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -248,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto piece_mem = [&](int i) { return reinterpret_cast<Piece*>(smem + OFF_PIECE + (i % kPieces) * 64); };
   int* start = reinterpret_cast<int*>(smem + OFF_START);
+  int2* seen = reinterpret_cast<int2*>(smem + OFF_SEEN);
   const uint32_t bar0 = ptx::smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -278,29 +320,35 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kWarpTma && lane < 6)
     ptx::prefetch_tmap(lane == 0 ? &tmQp : lane == 1 ? &tmQs : lane == 2 ? &tmKp : lane == 3 ? &tmVp : lane == 4 ? &tmKs : &tmVs);
   pdl_wait();  // lengths, q and the caches may come from the previous kernel
-  fill_starts(a, start, warp, lane);
+  fill_tables(a, start, seen, warp, lane);
   const int bins = a.bins_p + a.bins_s, total = start[bins];
-  if (blockIdx.x == 0) {  // for the joining kernel; lengths out of range are reported once
-    for (int i = threadIdx.x; i <= bins; i += kThreads) a.starts[i] = start[i];
-    bool bad = false;
-    if (a.P_max > 0)
-      for (int g = threadIdx.x; g < a.G; g += kThreads) bad |= (unsigned)a.prefix_lens[g] > (unsigned)a.P_max;
-    if (a.S_max > 0)
-      for (int b = threadIdx.x; b < a.B; b += kThreads) bad |= (unsigned)a.suffix_lens[b] > (unsigned)a.S_max;
-    if (bad) atomicOr(a.status, kStatusData);
-  }
   const int share = share_of(a, total);
   const long long v_begin = (long long)blockIdx.x * share;
-  if (v_begin >= total) return;
-  const int v0 = (int)v_begin, v1 = (int)min(v_begin + share, (long long)total);
-  if (warp == kWarpMma) {
+  const bool works = v_begin < total;
+  const int v0 = (int)min(v_begin, (long long)total), v1 = (int)min(v_begin + share, (long long)total);
+  if (works && warp == kWarpMma) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
-  __syncthreads();
+  if (warp < 4) {  // while the first copies are on their way
+    const int units_p = a.P_max > 0 ? a.G * a.Hkv * a.tiles_p : 0, units_s = a.S_max > 0 ? a.B * a.Hkv * a.tiles_s : 0;
+    for (int u = blockIdx.x * 128 + threadIdx.x; u < units_p + units_s; u += a.ctas * 128)
+      a.pieces[u] = unit_pieces(a, start, seen, share, u >= units_p, u >= units_p ? u - units_p : u);
+  }
+  if (blockIdx.x + 1 == gridDim.x && warp < 4) {  // lengths out of range are reported once
+    bool bad = false;
+    if (a.P_max > 0)
+      for (int g = threadIdx.x; g < a.G; g += 128) bad |= (unsigned)a.prefix_lens[g] > (unsigned)a.P_max;
+    if (a.S_max > 0)
+      for (int b = threadIdx.x; b < a.B; b += 128) bad |= (unsigned)a.suffix_lens[b] > (unsigned)a.S_max;
+    if (bad) atomicOr(a.status, kStatusData);
+  }
+  if (!works) return;
+  // warp 4 needs neither tensor memory nor this
+  if (warp != kWarpTma) asm volatile("bar.sync 1, 160;" ::: "memory");
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = warp != kWarpTma ? *tmem_slot : 0u;
   auto sSlot = [&](int s) { return ptx::smem_u32(smem + OFF_SLOT + s * SLOT_BYTES); };
   const uint32_t sQ = ptx::smem_u32(smem);
   const int R = a.H / a.Hkv;
@@ -324,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       p.nt = 0;
       while (v < v1 && p.nt == 0) {
         int next;
-        p = piece_at(a, start, v, v1, lane, &next);
+        p = piece_at(a, start, seen, v, v1, &next);
         v = next;
       }
       if (lane == 0) {
@@ -462,7 +510,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int nrows = p.ntok * R;
       const bool live = (int)threadIdx.x < nrows, warp_live = warp * 32 < nrows;
       // keys [lo, hi) that this row sees, from the side's first key
-      int lo = 0, hi = 0;
+      // (a thread without a row masks nothing: no one reads its weights)
+      int lo = 0, hi = 0x7fffffff;
       const int token = p.tok0 + (int)threadIdx.x / R;
       if (live) {
         const int b = token / a.Tq;
@@ -508,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[i + k]);
           const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           // the running max moves only when it grows by more than 2^8
-          const bool rescale = (tmax - m_run) * c > kRescaleThreshold;
+          const bool rescale = live && (tmax - m_run) * c > kRescaleThreshold;
           const float m_new = rescale ? tmax : m_run;
           const float mc = m_new == -INFINITY ? 0.f : m_new * c;
           uint32_t pk[32];
@@ -575,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       ptx::tc_fence_after();
       if (warp_live) {
-        const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
+        const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
         const long long prow = (long long)p.slot * ((p.suffix ? a.box_s : a.box_p) * R) + threadIdx.x;
         float* dst = (p.suffix ? a.part_os : a.part_op) + prow * kD;
 #pragma unroll 1
@@ -620,69 +669,52 @@ __global__ void __launch_bounds__(128) k_prefix_combine(const PrefixAttnArgs a) 
   const int lane = threadIdx.x & 31;
   if (row >= (long long)a.B * a.Tq * a.H) return;
   const int R = a.H / a.Hkv, token = (int)(row / a.H), h = (int)(row % a.H), hk = h / R;
-  const int share = share_of(a, a.starts[a.bins_p + a.bins_s]);
-  // the row's pieces on either side: slots [first, first + count) and its row in each
-  long long first[2] = {0, 0};
-  int count[2] = {0, 0}, tr[2] = {0, 0};
+  // the row's unit on either side, and its row in the unit's tile
+  int2 in_p = make_int2(0, 0), in_s = make_int2(0, 0);
+  int rp = 0, rs = 0;
   if (a.P_max > 0) {
-    const int g = token / (a.rows_per_group * a.Tq), it = token % (a.rows_per_group * a.Tq), tt = it / a.box_p;
-    int at = a.starts[g / a.bin_p], t0;
-    for (int i = g / a.bin_p * a.bin_p; i < g; ++i)
-      at += a.Hkv * a.tiles_p * unit_cost(unit_tiles(a, prefix_seq(a, i, lane), 0, 0, &t0));
-    const int tiles = unit_tiles(a, prefix_seq(a, g, lane), 0, 0, &t0);
-    at += (hk * a.tiles_p + tt) * unit_cost(tiles) + kUnitCost;
-    if (tiles > 0) {
-      first[0] = (g * a.Hkv + hk) * a.tiles_p + tt + at / share;
-      count[0] = (at + tiles - 1) / share - at / share + 1;
-    }
-    tr[0] = it % a.box_p * R + h % R;
+    const int per = a.rows_per_group * a.Tq, g = token / per, it = token % per;
+    in_p = a.pieces[(g * a.Hkv + hk) * a.tiles_p + it / a.box_p];
+    rp = it % a.box_p * R + h % R;
   }
   if (a.S_max > 0) {
-    const int b = token / a.Tq, it = token % a.Tq, tt = it / a.box_s;
-    int at = a.starts[a.bins_p + b / a.bin_s], t0;
-    for (int i = b / a.bin_s * a.bin_s; i < b; ++i) at += a.Hkv * suffix_cost(a, suffix_seq(a, i));
-    const Seq s = suffix_seq(a, b);
-    at += hk * suffix_cost(a, s) + kUnitCost;
-    for (int i = 0; i < tt; ++i) at += unit_cost(unit_tiles(a, s, 1, i, &t0));
-    const int tiles = unit_tiles(a, s, 1, tt, &t0);
-    if (tiles > 0) {
-      first[1] = (b * a.Hkv + hk) * a.tiles_s + tt + at / share;
-      count[1] = (at + tiles - 1) / share - at / share + 1;
-    }
-    tr[1] = it % a.box_s * R + h % R;
+    const int b = token / a.Tq, it = token % a.Tq;
+    in_s = a.pieces[(a.P_max > 0 ? a.G * a.Hkv * a.tiles_p : 0) + (b * a.Hkv + hk) * a.tiles_s + it / a.box_s];
+    rs = it % a.box_s * R + h % R;
   }
-  const int parts = count[0] + count[1];
-  auto place = [&](int p, const float** lse, const float** o) {
-    const int side = p >= count[0];
-    const long long r = (first[side] + p - (side ? count[0] : 0)) * ((side ? a.box_s : a.box_p) * R) + tr[side];
-    *lse = (side ? a.part_ls : a.part_lp) + r;
-    *o = (side ? a.part_os : a.part_op) + r * kD;
-  };
-  float m = -INFINITY;
-  for (int p = lane; p < parts; p += 32) {
-    const float *l, *o;
-    place(p, &l, &o);
-    m = fmaxf(m, *l);
-  }
-  m = warp_max(m);
+  const int parts = in_p.y + in_s.y;
+  float m = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  if (m != -INFINITY) {
-    for (int p = 0; p < parts; ++p) {
-      const float *lp, *op;
-      place(p, &lp, &op);
-      const float l = *lp;
-      if (l == -INFINITY) continue;
-      const float w = ex2((l - m) * 1.4426950408889634f);
-      const float4 o = *reinterpret_cast<const float4*>(op + 4 * lane);
-      acc.x += w * o.x, acc.y += w * o.y, acc.z += w * o.z, acc.w += w * o.w;
-      sum += w;
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    // lane p holds piece p0 + p: its weight, and where its output row is
+    const int p = p0 + lane, n = min(32, parts - p0);
+    float l = -INFINITY;
+    const float* o = a.part_op;
+    if (p < parts) {
+      const bool side = p >= in_p.y;
+      const long long r = side ? (long long)(in_s.x + p - in_p.y) * (a.box_s * R) + rs : (long long)(in_p.x + p) * (a.box_p * R) + rp;
+      l = (side ? a.part_ls : a.part_lp)[r];
+      o = (side ? a.part_os : a.part_op) + r * kD;
     }
-    const float inv = 1.0f / sum;
-    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+    const float m_new = fmaxf(m, warp_max(l));
+    if (m_new == -INFINITY) continue;
+    const float w = ex2((l - m_new) * 1.4426950408889634f), old = ex2((m - m_new) * 1.4426950408889634f);
+    m = m_new;
+    sum = sum * old + warp_sum(w);
+    acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* oi = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), i));
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wi != 0.f) x = *reinterpret_cast<const float4*>(oi + 4 * lane);  // a piece of weight 0 may have no output
+      acc.x += wi * x.x, acc.y += wi * x.y, acc.z += wi * x.z, acc.w += wi * x.w;
+    }
   }
-  *reinterpret_cast<uint2*>(a.out + row * kD + 4 * lane) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-  if (lane == 0 && a.out_lse != nullptr) a.out_lse[row] = m == -INFINITY ? m : m + logf(sum);
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  *reinterpret_cast<uint2*>(a.out + row * kD + 4 * lane) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lane == 0 && a.out_lse != nullptr) a.out_lse[row] = sum == 0.f ? m : m + logf(sum);
 }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -733,8 +765,8 @@ bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes) {
   a->off_os = rows_p * kD * 4;
   a->off_lp = a->off_os + rows_s * kD * 4;
   a->off_ls = a->off_lp + align(rows_p * 4);
-  a->off_starts = a->off_ls + align(rows_s * 4);
-  *bytes = a->off_starts + align((2 * kMaxBins + 2) * 4);
+  a->off_pieces = a->off_ls + align(rows_s * 4);
+  *bytes = a->off_pieces + align((size_t)(units_p + units_s) * 8);
   return true;
 }
 
@@ -747,7 +779,7 @@ bool launch_prefix_attn(const PrefixAttnArgs& args, const void* q, long long ldq
   a.part_os = reinterpret_cast<float*>(ws + a.off_os);
   a.part_lp = reinterpret_cast<float*>(ws + a.off_lp);
   a.part_ls = reinterpret_cast<float*>(ws + a.off_ls);
-  a.starts = reinterpret_cast<int*>(ws + a.off_starts);
+  a.pieces = reinterpret_cast<int2*>(ws + a.off_pieces);
   CUtensorMap m[6];
   const int tokens = a.B * a.Tq, R = a.H / a.Hkv;
   if (!q_map(&m[0], q, ldq, tokens, a.H, R, a.box_p) || !q_map(&m[1], q, ldq, tokens, a.H, R, a.box_s)) return false;

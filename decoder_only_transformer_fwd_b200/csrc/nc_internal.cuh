@@ -237,10 +237,11 @@ struct PrefixAttnArgs {
   // filled by prefix_attn_plan(): query tokens per tile and tiles per sequence
   // (prefix, suffix), sequences per bin and bins of the tables of starts
   int rows_per_group, ctas, box_p, box_s, tiles_p, tiles_s, bin_p, bin_s, bins_p, bins_s;
-  size_t off_os, off_lp, off_ls, off_starts;
-  // workspace: pieces' outputs and log-sum-exps, prefix and suffix; the tables
+  size_t off_os, off_lp, off_ls, off_pieces;
+  // workspace: pieces' outputs and log-sum-exps, prefix and suffix; where each
+  // unit's pieces are (first slot, count)
   float *part_op, *part_os, *part_lp, *part_ls;
-  int* starts;
+  int2* pieces;
 };
 // false where a count does not fit an int
 bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes);
