@@ -14,14 +14,19 @@
 // per row.  What bounds it: reading the caches from HBM, as long as a key
 // head has fewer than about 250 query rows per group.
 //
-// The work is a sequence of units, prefix units (group, key head, 128-row query
-// tile) and then suffix units (row, key head, query tile), each a run of
-// 64-key tiles.  The CTAs cut the sequence of all tiles into equal shares, as
-// the lengths in memory give them: a long unit is spread over many CTAs, a CTA
-// takes many short ones, and all finish together.  What a CTA does of a unit is
-// a piece; it leaves its rows' normalised output (fp32) and log-sum-exp in the
-// workspace, at slot (unit + CTA), which no two pieces share.
-// k_prefix_combine joins a row's pieces with weights exp(lse_piece - lse).
+// The work of a key head is a sequence of units, prefix units (group, 128-row
+// query tile) and then suffix units (row, query tile), each a run of 64-key
+// tiles.  Neighbouring CTAs take neighbouring heads (or, with many heads, bands
+// of heads), and the CTAs of a band cut its sequence of tiles into equal shares,
+// as the lengths in memory give them: a long unit is spread over many CTAs, a
+// CTA takes many short ones, all finish together, and the heads' keys of one
+// token, which lie side by side in memory, are read at the same time (64 rows,
+// 12 heads, 32768 keys, attention kernel alone: 46 us with the heads one after
+// the other, 40 us with one head's keys contiguous).
+// What a CTA does of a unit is a piece; it leaves its rows' normalised output
+// (fp32) and log-sum-exp in the workspace, at slot (unit + CTA of the band),
+// which no two pieces share.  k_prefix_combine joins a row's pieces with weights
+// exp(lse_piece - lse).
 //
 // A CTA: warps 0..3 softmax (one row per thread = TMEM lane), warp 4 cuts the
 // pieces and issues the copies (TMA), warp 5 MMA.  Warp 4 runs ahead: the next
@@ -62,6 +67,7 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.6931471805599453f;
 // What a unit costs besides its tiles (query load, set-up, rows out), in tiles.
 constexpr int kUnitCost = 1;
+constexpr int kPrefixSplitRows = 4096;
 
 struct Piece {
   int suffix, seq, hk;  // side, group or row, key head
@@ -142,14 +148,14 @@ __device__ void fill_tables(const PrefixAttnArgs& a, int* start, int2* seen, int
     for (int g = i * a.bin_p; g < min(a.G, (i + 1) * a.bin_p); ++g) {
       const int least = windowed(a) ? __reduce_min_sync(0xffffffffu, least_suffix(a, g, lane, 32)) : 0;
       const Seq s = prefix_seq(a, g, least);
-      c += a.Hkv * a.tiles_p * unit_cost(unit_tiles(a, s, 0, 0, &t0));
+      c += a.band * a.tiles_p * unit_cost(unit_tiles(a, s, 0, 0, &t0));
       if (lane == 0 && a.bin_p == 1) seen[g] = make_int2(s.lo, s.hi);
     }
     if (lane == 0) start[i] = c;
   }
   for (int i = threadIdx.x; i < a.bins_s; i += kThreads) {
     int c = 0;
-    for (int b = i * a.bin_s; b < min(a.B, (i + 1) * a.bin_s); ++b) c += a.Hkv * suffix_cost(a, suffix_seq(a, b));
+    for (int b = i * a.bin_s; b < min(a.B, (i + 1) * a.bin_s); ++b) c += a.band * suffix_cost(a, suffix_seq(a, b));
     start[a.bins_p + i] = c;
   }
   __syncthreads();
@@ -184,9 +190,14 @@ __device__ __forceinline__ Seq group_seq(const PrefixAttnArgs& a, const int2* se
   return s;
 }
 
-// share of the total cost that a CTA takes
+// share of a band's total cost that a CTA takes
 __device__ __forceinline__ int share_of(const PrefixAttnArgs& a, int total) {
-  return max((total + a.ctas - 1) / a.ctas, kUnitCost + 1);
+  return max((total + a.per_band - 1) / a.per_band, kUnitCost + 1);
+}
+
+// slot of what CTA `cta` of band b does of the band's unit u
+__device__ __forceinline__ int slot_of(const PrefixAttnArgs& a, int suffix, int b, int u, int cta) {
+  return b * ((suffix ? a.B * a.tiles_s : a.G * a.tiles_p) * a.band + a.per_band) + u + cta;
 }
 
 // The piece that holds cost position v, as far as `end`; *next: the position
@@ -207,11 +218,11 @@ __device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, const int2*
     for (p.seq = lo * a.bin_p;; ++p.seq) {
       s = group_seq(a, seen, p.seq);
       tiles = unit_tiles(a, s, 0, 0, &t0);
-      const int all = a.Hkv * a.tiles_p * unit_cost(tiles);
+      const int all = a.band * a.tiles_p * unit_cost(tiles);
       if (at < all || p.seq + 1 >= a.G) break;
       at -= all;
     }
-    const int u = min(at / max(unit_cost(tiles), 1), a.Hkv * a.tiles_p - 1);
+    const int u = min(at / max(unit_cost(tiles), 1), a.band * a.tiles_p - 1);
     at -= u * unit_cost(tiles);
     p.hk = u / a.tiles_p;
     tt = u % a.tiles_p;
@@ -220,10 +231,10 @@ __device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, const int2*
     for (p.seq = (lo - a.bins_p) * a.bin_s;; ++p.seq) {
       s = suffix_seq(a, p.seq);
       one = suffix_cost(a, s);
-      if (at < a.Hkv * one || p.seq + 1 >= a.B) break;
-      at -= a.Hkv * one;
+      if (at < a.band * one || p.seq + 1 >= a.B) break;
+      at -= a.band * one;
     }
-    p.hk = min(at / max(one, 1), a.Hkv - 1);
+    p.hk = min(at / max(one, 1), a.band - 1);
     at -= p.hk * one;
     for (tt = 0;; ++tt) {
       tiles = unit_tiles(a, s, 1, tt, &t0);
@@ -241,29 +252,34 @@ __device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, const int2*
   const int tokens = (p.suffix ? 1 : a.rows_per_group) * a.Tq, box = p.suffix ? a.box_s : a.box_p;
   p.tok0 = p.seq * tokens + tt * box;
   p.ntok = min(box, tokens - tt * box);
-  p.slot = (p.seq * a.Hkv + p.hk) * (p.suffix ? a.tiles_s : a.tiles_p) + tt + blockIdx.x;
+  const int b = blockIdx.x % a.bands;
+  p.slot = slot_of(a, p.suffix, b, (p.seq * a.band + p.hk) * (p.suffix ? a.tiles_s : a.tiles_p) + tt, blockIdx.x / a.bands);
+  p.hk += b * a.band;
   return p;
 }
 
-// Where the pieces of unit u of a side lie, for k_prefix_combine: (first slot,
-// count) = (u + first CTA, CTAs that hold one of its tiles).
+// Where the pieces of unit u of a side lie, for k_prefix_combine: first slot and
+// number of CTAs that hold one of its tiles.  Units are numbered by sequence, key
+// head, query tile.
 __device__ int2 unit_pieces(const PrefixAttnArgs& a, const int* start, const int2* seen, int share, int suffix, int u) {
   const int tiles_q = suffix ? a.tiles_s : a.tiles_p, bin = suffix ? a.bin_s : a.bin_p;
   const int tt = u % tiles_q, hk = u / tiles_q % a.Hkv, seq = u / tiles_q / a.Hkv, i0 = seq / bin * bin;
+  const int b = hk / a.band, hb = hk % a.band;  // band, head within it
   int at = start[(suffix ? a.bins_p : 0) + seq / bin] + kUnitCost, t0, tiles;
   if (!suffix) {
-    for (int i = i0; i < seq; ++i) at += a.Hkv * a.tiles_p * unit_cost(unit_tiles(a, group_seq(a, seen, i), 0, 0, &t0));
+    for (int i = i0; i < seq; ++i) at += a.band * a.tiles_p * unit_cost(unit_tiles(a, group_seq(a, seen, i), 0, 0, &t0));
     tiles = unit_tiles(a, group_seq(a, seen, seq), 0, 0, &t0);
-    at += (hk * a.tiles_p + tt) * unit_cost(tiles);
+    at += (hb * a.tiles_p + tt) * unit_cost(tiles);
   } else {
-    for (int i = i0; i < seq; ++i) at += a.Hkv * suffix_cost(a, suffix_seq(a, i));
+    for (int i = i0; i < seq; ++i) at += a.band * suffix_cost(a, suffix_seq(a, i));
     const Seq s = suffix_seq(a, seq);
-    at += hk * suffix_cost(a, s);
+    at += hb * suffix_cost(a, s);
     for (int i = 0; i < tt; ++i) at += unit_cost(unit_tiles(a, s, 1, i, &t0));
     tiles = unit_tiles(a, s, 1, tt, &t0);
   }
   if (tiles == 0) return make_int2(0, 0);
-  return make_int2(u + at / share, (at + tiles - 1) / share - at / share + 1);
+  return make_int2(slot_of(a, suffix, b, (seq * a.band + hb) * tiles_q + tt, at / share),
+                   (at + tiles - 1) / share - at / share + 1);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -323,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   fill_tables(a, start, seen, warp, lane);
   const int bins = a.bins_p + a.bins_s, total = start[bins];
   const int share = share_of(a, total);
-  const long long v_begin = (long long)blockIdx.x * share;
+  const long long v_begin = (long long)(blockIdx.x / a.bands) * share;
   const bool works = v_begin < total;
   const int v0 = (int)min(v_begin, (long long)total), v1 = (int)min(v_begin + share, (long long)total);
   if (works && warp == kWarpMma) {
@@ -661,12 +677,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Joins a row's pieces: one warp per row, four columns per lane.
+// Joins a row's pieces: WPR warps per row, four columns per lane; warp w takes
+// every WPR-th piece and the warps' sums are joined in shared memory.
+template <int WPR>
 __global__ void __launch_bounds__(128) k_prefix_combine(const PrefixAttnArgs a) {
+  __shared__ float4 s_acc[WPR > 1 ? WPR : 1][32];
+  __shared__ float s_m[WPR], s_sum[WPR];
   pdl_launch_dependents();
   pdl_wait();
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);  // token-major, then head
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = WPR > 1 ? warp : 0;
+  const long long row = WPR > 1 ? (long long)blockIdx.x : (long long)blockIdx.x * 4 + warp;  // token-major, then head
   if (row >= (long long)a.B * a.Tq * a.H) return;
   const int R = a.H / a.Hkv, token = (int)(row / a.H), h = (int)(row % a.H), hk = h / R;
   // the row's unit on either side, and its row in the unit's tile
@@ -685,9 +705,9 @@ __global__ void __launch_bounds__(128) k_prefix_combine(const PrefixAttnArgs a) 
   const int parts = in_p.y + in_s.y;
   float m = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    // lane p holds piece p0 + p: its weight, and where its output row is
-    const int p = p0 + lane, n = min(32, parts - p0);
+  for (int p0 = w0; p0 < parts; p0 += 32 * WPR) {
+    // lane i holds piece p0 + WPR i: its weight, and where its output row is
+    const int p = p0 + WPR * lane, n = min(32, (parts - p0 + WPR - 1) / WPR);
     float l = -INFINITY;
     const float* o = a.part_op;
     if (p < parts) {
@@ -702,14 +722,40 @@ __global__ void __launch_bounds__(128) k_prefix_combine(const PrefixAttnArgs a) 
     m = m_new;
     sum = sum * old + warp_sum(w);
     acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* oi = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), i));
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (wi != 0.f) x = *reinterpret_cast<const float4*>(oi + 4 * lane);  // a piece of weight 0 may have no output
-      acc.x += wi * x.x, acc.y += wi * x.y, acc.z += wi * x.z, acc.w += wi * x.w;
+    // four rows in flight; a piece of weight 0 may have left none (whatever is
+    // there is read and not used)
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      float4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned long long oi = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), min(i0 + i, n - 1));
+        x[i] = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(oi) + 4 * lane);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float wi = i0 + i < n ? __shfl_sync(0xffffffffu, w, i0 + i) : 0.f;
+        if (wi != 0.f) acc.x += wi * x[i].x, acc.y += wi * x[i].y, acc.z += wi * x[i].z, acc.w += wi * x[i].w;
+      }
     }
+  }
+  if (WPR > 1) {
+    s_acc[warp][lane] = acc;
+    if (lane == 0) s_m[warp] = m, s_sum[warp] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+    float top = s_m[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) top = fmaxf(top, s_m[i]);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) {
+      const float w = s_m[i] == -INFINITY ? 0.f : ex2((s_m[i] - top) * 1.4426950408889634f);
+      const float4 x = s_acc[i][lane];
+      acc.x += w * x.x, acc.y += w * x.y, acc.z += w * x.z, acc.w += w * x.w;
+      sum += w * s_sum[i];
+    }
+    m = top;
   }
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   *reinterpret_cast<uint2*>(a.out + row * kD + 4 * lane) =
@@ -742,7 +788,19 @@ bool kv_map(CUtensorMap* m, const void* p, long long ld, long long ls, int seqs,
 bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes) {
   const int R = a->H / a->Hkv;
   a->rows_per_group = a->B / a->G;
-  a->ctas = kPrefixCtas;
+  // Bands of heads: as narrow as leaves at most 5% of the CTAs without work
+  // (12 heads: 12 bands of 24 CTAs; 100 heads: 25 bands of 11), or the best.
+  int used = 0;
+  for (int band = 1; band <= a->Hkv; ++band) {
+    if (a->Hkv % band != 0 || a->Hkv / band > kPrefixCtas) continue;
+    const int bands = a->Hkv / band, per = kPrefixCtas / bands;
+    if (bands * per > used) {
+      used = bands * per;
+      a->band = band, a->bands = bands, a->per_band = per;
+    }
+    if (20 * used >= 19 * kPrefixCtas) break;
+  }
+  a->ctas = a->bands * a->per_band;
   const int fit = kRows / R;  // tokens whose query rows fit a tile
   const long long tok_p = (long long)a->rows_per_group * a->Tq;
   a->box_p = (int)(fit < tok_p ? fit : tok_p);
@@ -760,7 +818,7 @@ bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes) {
   if (units_p > most || units_s > most) return false;
   if (units_p * (ceil_div(a->P_max, kKeys) + kUnitCost) + units_s * (ceil_div(a->S_max, kKeys) + kUnitCost) > most) return false;
   auto align = [](size_t b) { return (b + 255) & ~size_t(255); };
-  const size_t rows_p = units_p > 0 ? (size_t)(units_p + a->ctas) * (a->box_p * R) : 0;
+  const size_t rows_p = units_p > 0 ? (size_t)(units_p + a->ctas) * (a->box_p * R) : 0;  // a slot per unit and CTA
   const size_t rows_s = units_s > 0 ? (size_t)(units_s + a->ctas) * (a->box_s * R) : 0;
   a->off_os = rows_p * kD * 4;
   a->off_lp = a->off_os + rows_s * kD * 4;
@@ -797,7 +855,9 @@ bool launch_prefix_attn(const PrefixAttnArgs& args, const void* q, long long ldq
   }
   const long long rows = (long long)tokens * a.H;
   LaunchScope scope_(KK_PREFIX_ATTN, st);
-  return launch_pdl(k_prefix_combine, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, a) == cudaSuccess;
+  // few rows: their pieces are spread over four warps
+  if (rows <= kPrefixSplitRows) return launch_pdl(k_prefix_combine<4>, dim3((unsigned)rows), dim3(128), 0, st, 1, a) == cudaSuccess;
+  return launch_pdl(k_prefix_combine<1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, a) == cudaSuccess;
 }
 
 }  // namespace nc
