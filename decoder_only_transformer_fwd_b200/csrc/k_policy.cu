@@ -14,9 +14,13 @@
 // whole gradient row.
 //
 // HBM bound: the logits in once, the gradient out once (2 V elements per
-// token).  A CTA takes a row at a time: one pass with a running maximum and
-// sum, then a second pass that reads the row again (from L2, where the first
-// pass left it) and writes the gradient.
+// token).  Two forms, by a row's bytes:
+//   k_policy_loss  rows up to 32 KB: a CTA takes a row at a time, one pass with
+//     a running maximum and sum, then a second pass that reads the row again
+//     (from L2, where the first pass left it) and writes the gradient.  Several
+//     CTAs per SM cover each other's latencies.
+//   k_policy_ring  longer rows: bulk copies bring a row into a shared-memory
+//     ring, both passes read it there, and the next row's copies run meanwhile.
 #include <cfloat>
 
 #include "nc_internal.cuh"
@@ -26,8 +30,6 @@ namespace nc {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kCtasPerSm = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp_diff(float z, float m) {
@@ -82,160 +84,227 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   return v;
 }
 
-struct Scratch {
-  float m[kThreads / 32];
-  double s[kThreads / 32];
-  float coef, gz, top;  // of the row: -gz / S, gz = w dL/dlp, max
+// e^d - d - 1 without cancellation: its series where the terms fall fast
+// (|d| <= 1/2: the first one left out is 2^-28 of the sum), else from expm1
+__device__ __forceinline__ float exp_excess(float d) {
+  if (fabsf(d) > 0.5f) return expm1f(d) - d;
+  float s = 1.0f / 3628800;
+  s = fmaf(s, d, 1.0f / 362880);
+  s = fmaf(s, d, 1.0f / 40320);
+  s = fmaf(s, d, 1.0f / 5040);
+  s = fmaf(s, d, 1.0f / 720);
+  s = fmaf(s, d, 1.0f / 120);
+  s = fmaf(s, d, 1.0f / 24);
+  s = fmaf(s, d, 1.0f / 6);
+  s = fmaf(s, d, 0.5f);
+  return s * d * d;
+}
+
+// what a token's row leaves: dL/dz_v = coef e^{z_v - top} + gz [v = y]
+struct Row {
+  float coef, gz;
+  double lp, loss, kl, clipped;  // the last three weighted
 };
+
+// From the row's maximum m and sum S of e^{z - m}.  count: tokens (norm 0) or
+// sequences with a target; tokens: those of the token's sequence.
+__device__ __forceinline__ Row row_terms(const PolicyArgs& a, float zy, float m, double S, float adv, float old, float ref,
+                                         int count, int tokens) {
+  Row t;
+  t.lp = (double)zy - (double)m - log(S);
+  const double w = a.norm == 0 ? 1.0 / count : 1.0 / ((double)count * tokens);
+  const double A = (double)adv, x = a.old_logp != nullptr ? t.lp - (double)old : 0.0;
+  const bool cut = (A > 0.0 && x > a.log_high) || (A < 0.0 && x < a.log_low);
+  // with the branch decided, fp32 does: the exponents are differences
+  const double r = (double)expf((float)x);
+  double loss = -(cut ? (A > 0.0 ? a.ratio_high : a.ratio_low) : r) * A, slope = cut ? 0.0 : -r * A, kl = 0.0;
+  if (a.ref_logp != nullptr) {
+    const float d = (float)((double)ref - t.lp);
+    kl = (double)exp_excess(d);
+    loss += (double)a.kl_beta * kl;
+    slope -= (double)a.kl_beta * (kl + (double)d);
+  }
+  t.loss = w * loss;
+  t.kl = w * kl;
+  t.clipped = cut ? w : 0.0;
+  t.gz = (float)(w * slope);
+  t.coef = (float)(-(w * slope) / S);
+  return t;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// e^{f - top} of a pair, in packed fp32 (the special-function unit's rate of 16
+// a clock bounds both passes, so the rest is kept short)
+__device__ __forceinline__ float2 exp_pair(float2 f, float2 neg_top) {
+  const float2 x = __fmul2_rn(__fadd2_rn(f, neg_top), make_float2(kLog2e, kLog2e));
+  return make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+}
 
 struct Online {
   float m = -FLT_MAX, s = 0.f;
+  __device__ __forceinline__ void add1(float f) {
+    const float t = fmaxf(m, f);
+    s = s * exp_diff(m, t) + exp_diff(f, t);
+    m = t;
+  }
   template <int N>
   __device__ __forceinline__ void add(const float (&f)[N]) {
     float t = m;
 #pragma unroll
-    for (int i = 0; i < N; ++i) t = fmaxf(t, f[i]);
-    float e = 0.f;
+    for (int i = 0; i < N; i += 2) t = max3(t, f[i], f[i + 1]);
+    const float2 nt = make_float2(-t, -t);
+    float2 e = make_float2(s * exp_diff(m, t), 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) e += exp_diff(f[i], t);
-    s = s * exp_diff(m, t) + e;
+    for (int i = 0; i < N; i += 2) e = __fadd2_rn(e, exp_pair(make_float2(f[i], f[i + 1]), nt));
+    s = e.x + e.y;
     m = t;
   }
 };
 
 __device__ __forceinline__ bool valid(int y, int V) { return (unsigned)y < (unsigned)V; }
 
+// tokens (norm 0) or sequences (norm 1) with a target, by the block's threads
+// first .. first + threads - 1; this thread's share of the sum
+__device__ __forceinline__ int count_share(const PolicyArgs& a, int tid, int threads) {
+  int n = 0;
+  if (a.norm == 0) {
+    const int M = a.B * a.T;
+    for (int i = tid; i < M; i += threads) n += valid(a.targets[i], a.V);
+  } else {
+    const int lane = tid & 31;
+    for (int b = tid >> 5; b < a.B; b += threads >> 5) {
+      bool any = false;
+      for (int t0 = 0; t0 < a.T && !any; t0 += 32)
+        any = __any_sync(0xffffffffu, t0 + lane < a.T && valid(a.targets[(size_t)b * a.T + t0 + lane], a.V));
+      n += lane == 0 && any;
+    }
+  }
+  return n;
+}
+
+// 16 bytes of the gradient, from element v0 of the row on
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_policy_loss(const PolicyArgs a, double* part) {
-  __shared__ Scratch sh;
+__device__ __forceinline__ void grad_quad(float (&f)[Quad<T>::N], int v0, int y, const Row& t, float top) {
+  const float2 nt = make_float2(-top, -top), c = make_float2(t.coef, t.coef);
+#pragma unroll
+  for (int e = 0; e < Quad<T>::N; e += 2) {
+    const float2 g = __fmul2_rn(exp_pair(make_float2(f[e], f[e + 1]), nt), c);
+    f[e] = g.x;
+    f[e + 1] = g.y;
+  }
+  if ((unsigned)(y - v0) < (unsigned)Quad<T>::N) {
+#pragma unroll
+    for (int e = 0; e < Quad<T>::N; ++e) f[e] += v0 + e == y ? t.gz : 0.f;
+  }
+}
+
+// A row without a target: zeros.
+template <typename T>
+__device__ __forceinline__ void zero_row(T* dz, int V, int tid, int threads) {
+  const int head = head_of(dz, V), nq = (V - head) / Quad<T>::N, tail = head + nq * Quad<T>::N;
+  if (tid < head) Act<T>::st(dz + tid, 0.f);
+  if (tail + tid < V) Act<T>::st(dz + tail + tid, 0.f);
+  float f[Quad<T>::N] = {};
+  for (int i = tid; i < nq; i += threads) Quad<T>::st(dz + head + (size_t)i * Quad<T>::N, f);
+}
+
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const PolicyArgs a, double* part) {
+  __shared__ float s_m[kThreads / 32];
+  __shared__ double s_s[kThreads / 32];
+  __shared__ Row s_row;
+  __shared__ float s_top;
   __shared__ int s_count;
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int M = a.B * a.T;
-  // tokens (norm 0) or sequences (norm 1) with a target, counted by every CTA
+  const int M = a.B * a.T, V = a.V;
   if (tid == 0) s_count = 0;
   __syncthreads();
-  {
-    int n = 0;
-    if (a.norm == 0) {
-      for (int i = tid; i < M; i += kThreads) n += valid(a.targets[i], a.V);
-    } else {
-      for (int b = warp; b < a.B; b += kThreads / 32) {
-        bool any = false;
-        for (int t0 = 0; t0 < a.T && !any; t0 += 32)
-          any = __any_sync(0xffffffffu, t0 + lane < a.T && valid(a.targets[(size_t)b * a.T + t0 + lane], a.V));
-        n += lane == 0 && any;
-      }
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0 && n != 0) atomicAdd(&s_count, n);
-  }
+  const int share = __reduce_add_sync(0xffffffffu, count_share(a, tid, kThreads));
+  if (lane == 0 && share != 0) atomicAdd(&s_count, share);
   __syncthreads();
   const int count = s_count;
   double sum_loss = 0.0, sum_kl = 0.0, sum_clip = 0.0;  // thread 0's
   for (int row = blockIdx.x; row < M; row += gridDim.x) {
     const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.ldl;
     T* dz = a.dlogits != nullptr ? static_cast<T*>(a.dlogits) + (size_t)row * a.lddl : nullptr;
-    const int V = a.V;
-    int y = a.targets[row];
-    if (y != -1 && !valid(y, V)) {  // recorded, and the token counts as padding
-      if (tid == 0) atomicOr(a.status, kStatusData);
-      y = -1;
+    const int y = a.targets[row];
+    if (!valid(y, V)) {  // no target, or a bad one: recorded, and the token counts as padding
+      if (tid == 0) {
+        a.out_logp[row] = 0.f;
+        if (y != -1) atomicOr(a.status, kStatusData);
+      }
+      if (dz != nullptr) zero_row(dz, V, tid, kThreads);
+      continue;
     }
-    float gz = 0.f, coef = 0.f, top = 0.f;
-    if (y >= 0) {
-      int tokens = count;
-      if (a.norm == 1) {
-        const int32_t* tg = a.targets + (size_t)(row / a.T) * a.T;
-        tokens = 0;
-        for (int t0 = 0; t0 < a.T; t0 += kThreads) tokens += __syncthreads_count(t0 + tid < a.T && valid(tg[t0 + tid], a.V));
-      }
-      const int head = head_of(z, V);
-      const int nq = (V - head) / Quad<T>::N;
-      Online o;
-      if (tid < head) {
-        const float f[1] = {Act<T>::ld(z + tid)};
-        o.add(f);
-      }
+    int tokens = count;
+    if (a.norm == 1) {
+      const int32_t* tg = a.targets + (size_t)(row / a.T) * a.T;
+      tokens = 0;
+      for (int t0 = 0; t0 < a.T; t0 += kThreads) tokens += __syncthreads_count(t0 + tid < a.T && valid(tg[t0 + tid], V));
+    }
+    const int head = head_of(z, V), nq = (V - head) / Quad<T>::N, tail = head + nq * Quad<T>::N;
+    Online o;
+    if (tid < head) o.add1(Act<T>::ld(z + tid));
+    if (tail + tid < V) o.add1(Act<T>::ld(z + tail + tid));
 #pragma unroll 4
-      for (int i = tid; i < nq; i += kThreads) {
-        float f[Quad<T>::N];
-        Quad<T>::ld(z + head + (size_t)i * Quad<T>::N, f);
-        o.add(f);
-      }
-      const int tail = head + nq * Quad<T>::N;
-      if (tail + tid < V) {
-        const float f[1] = {Act<T>::ld(z + tail + tid)};
-        o.add(f);
-      }
-      const float wm = warp_max(o.m);
-      const double ws = warp_sum_d((double)(o.s * exp_diff(o.m, wm)));
-      if (lane == 0) {
-        sh.m[warp] = wm;
-        sh.s[warp] = ws;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        const bool mine = lane < kThreads / 32;
-        const float m0 = mine ? sh.m[lane] : -FLT_MAX, m = warp_max(m0);
-        const double S = warp_sum_d(mine ? sh.s[lane] * (double)exp_diff(m0, m) : 0.0);
-        if (lane == 0) {
-          const double lp = (double)Act<T>::ld(z + y) - (double)m - log(S);
-          const double w = a.norm == 0 ? 1.0 / count : 1.0 / ((double)count * tokens);
-          const double A = (double)a.advantages[a.adv_per_token ? row : row / a.T];
-          const double x = a.old_logp != nullptr ? lp - (double)a.old_logp[row] : 0.0;
-          const bool over = A > 0.0 && x > a.log_high, under = A < 0.0 && x < a.log_low;
-          const double r = exp(x);
-          double loss = -(over ? a.ratio_high : (under ? a.ratio_low : r)) * A;
-          double slope = over || under ? 0.0 : -r * A;
-          double kl = 0.0;
-          if (a.ref_logp != nullptr) {
-            const double d = (double)a.ref_logp[row] - lp, em = expm1(d);
-            kl = em - d;
-            loss += (double)a.kl_beta * kl;
-            slope -= (double)a.kl_beta * em;
-          }
-          a.out_logp[row] = (float)lp;
-          sum_loss += w * loss;
-          sum_kl += w * kl;
-          sum_clip += over || under ? w : 0.0;
-          sh.gz = (float)(w * slope);
-          sh.coef = (float)(-(w * slope) / S);
-          sh.top = m;
-        }
-      }
-      __syncthreads();
-      gz = sh.gz, coef = sh.coef, top = sh.top;
-    } else if (tid == 0) {
-      a.out_logp[row] = 0.f;
+    for (int i = tid; i < nq; i += kThreads) {
+      float f[Quad<T>::N];
+      Quad<T>::ld(z + head + (size_t)i * Quad<T>::N, f);
+      o.add(f);
     }
+    const float wm = warp_max(o.m);
+    const double ws = warp_sum_d((double)(o.s * exp_diff(o.m, wm)));
+    if (lane == 0) {
+      s_m[warp] = wm;
+      s_s[warp] = ws;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const bool mine = lane < kThreads / 32;
+      const float m0 = mine ? s_m[lane] : -FLT_MAX, m = warp_max(m0);
+      const double S = warp_sum_d(mine ? s_s[lane] * (double)exp_diff(m0, m) : 0.0);
+      if (lane == 0) {
+        const Row t = row_terms(a, Act<T>::ld(z + y), m, S, a.advantages[a.adv_per_token ? row : row / a.T],
+                                a.old_logp != nullptr ? a.old_logp[row] : 0.f,
+                                a.ref_logp != nullptr ? a.ref_logp[row] : 0.f, count, tokens);
+        a.out_logp[row] = (float)t.lp;
+        sum_loss += t.loss;
+        sum_kl += t.kl;
+        sum_clip += t.clipped;
+        s_row = t;
+        s_top = m;
+      }
+    }
+    __syncthreads();
     if (dz != nullptr) {
+      const Row t = s_row;
+      const float top = s_top;
       // the gradient's own 16-byte boundaries; the logits at the same element
       // offsets when both rows start alike, else one element at a time
       const int head = head_of(dz, V);
       const bool alike = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
       const int nq = (V - head) / Quad<T>::N, tail = head + nq * Quad<T>::N;
-      auto one = [&](int v) { Act<T>::st(dz + v, y < 0 ? 0.f : coef * exp_diff(Act<T>::ld(z + v), top) + (v == y ? gz : 0.f)); };
+      auto one = [&](int v) { Act<T>::st(dz + v, t.coef * exp_diff(Act<T>::ld(z + v), top) + (v == y ? t.gz : 0.f)); };
       if (tid < head) one(tid);
       if (tail + tid < V) one(tail + tid);
 #pragma unroll 4
       for (int i = tid; i < nq; i += kThreads) {
         const int v0 = head + i * Quad<T>::N;
         float f[Quad<T>::N];
-        if (y >= 0) {
-          if (alike) {
-            Quad<T>::ld(z + v0, f);
-          } else {
-#pragma unroll
-            for (int e = 0; e < Quad<T>::N; ++e) f[e] = Act<T>::ld(z + v0 + e);
-          }
-#pragma unroll
-          for (int e = 0; e < Quad<T>::N; ++e) f[e] = coef * exp_diff(f[e], top) + (v0 + e == y ? gz : 0.f);
+        if (alike) {
+          Quad<T>::ld(z + v0, f);
         } else {
 #pragma unroll
-          for (int e = 0; e < Quad<T>::N; ++e) f[e] = 0.f;
+          for (int e = 0; e < Quad<T>::N; ++e) f[e] = Act<T>::ld(z + v0 + e);
         }
+        grad_quad<T>(f, v0, y, t, top);
         Quad<T>::st(dz + v0, f);
       }
     }
@@ -245,6 +314,225 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_policy_loss(const Poli
     part[3 * blockIdx.x] = sum_loss;
     part[3 * blockIdx.x + 1] = sum_kl;
     part[3 * blockIdx.x + 2] = sum_clip;
+  }
+}
+
+// Long rows.  Warps 0..15 work, warp 16 copies: a row's 16-byte words (up to 15
+// bytes at either end are read directly) in chunks of 16 KB, chunk n of the
+// CTA's sequence in slot n % NS.  Pass 1 leaves the row's last NS chunks where
+// they are; pass 2 takes those first and frees them, and then the ones before,
+// which were freed at once and are copied again (from L2).
+constexpr int kChunk = 16384, kWork = 512, kMeta = 16;
+template <int CPS> struct Ring {
+  static constexpr int NS = CPS == 1 ? 13 : 6;
+  static constexpr int SMEM = NS * kChunk + 1024;
+};
+
+template <typename T, int CPS>
+__global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArgs a, double* part) {
+  constexpr int NS = Ring<CPS>::NS, N = Quad<T>::N, kVec = kChunk / 16;
+  static_assert(NS <= kMeta, "a row has a chunk at least, so the copies run less than kMeta rows ahead");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  __shared__ uint64_t bars[2 * NS + 2];
+  __shared__ Row s_row[2];
+  __shared__ float s_top[2];
+  __shared__ int s_tokens[kMeta];
+  __shared__ float s_m[2][kWork / 32];
+  __shared__ double s_s[2][kWork / 32];
+  __shared__ int s_count;
+  __shared__ volatile int abort_flag;
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  auto full = [&](int n) { return bar0 + 8u * (n % NS); };
+  auto empty = [&](int n) { return bar0 + 8u * (NS + n % NS); };
+  const uint32_t red = bar0 + 8u * (2 * NS), ready = bar0 + 8u * (2 * NS + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int M = a.B * a.T, V = a.V;
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), kWork / 32);
+    }
+    ptx::mbar_init(red, kWork / 32);
+    ptx::mbar_init(ready, 1);
+    s_count = 0;
+    abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  __syncthreads();
+  pdl_wait();
+  const bool grad = a.dlogits != nullptr;
+  if (warp == kWork / 32) {
+    int n = 0, last_b = -1, tokens = 0, k = 0;
+    bool ok = true;
+    for (int row = blockIdx.x; ok && row < M; row += gridDim.x) {
+      if (!valid(a.targets[row], V)) continue;
+      if (a.norm == 1 && row / a.T != last_b) {
+        last_b = row / a.T;
+        int mine = 0;
+        for (int t = lane; t < a.T; t += 32) mine += valid(a.targets[(size_t)last_b * a.T + t], V);
+        tokens = __reduce_add_sync(0xffffffffu, mine);
+      }
+      const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.ldl;
+      const int head = head_of(z, V), nq = (V - head) / N, C = (nq + kVec - 1) / kVec;
+      const int again = grad && C > NS ? C - NS : 0;
+      if (lane == 0) {
+        s_tokens[k % kMeta] = tokens;
+        for (int i = 0; i < C + again; ++i, ++n) {
+          const int c = i < C ? i : i - C;
+          const uint32_t bytes = (uint32_t)min(kVec, nq - c * kVec) * 16u;
+          if (abort_flag || !ptx::mbar_wait(empty(n), ((uint32_t)(n / NS) & 1u) ^ 1u, a.status)) {
+            ok = false;
+            break;
+          }
+          ptx::mbar_arrive_expect_tx(full(n), bytes);
+          ptx::bulk_load(ptx::smem_u32(ring + (n % NS) * kChunk), z + head + (size_t)c * kVec * N, bytes, full(n));
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      ++k;
+    }
+    if (lane == 0) {
+      if (!ok) abort_flag = 1;
+      // every copy issued here has landed before the CTA may exit
+      for (int i = max(0, n - NS); i < n; ++i) ptx::mbar_wait(full(i), (uint32_t)(i / NS) & 1u, a.status);
+    }
+  } else {
+    const int share = __reduce_add_sync(0xffffffffu, count_share(a, tid, kWork));
+    if (lane == 0) {
+      if (share != 0) atomicAdd(&s_count, share);
+      ptx::mbar_arrive(red);
+    }
+    bool ok = ptx::mbar_wait(red, 0, a.status);
+    const int count = *(volatile int*)&s_count;
+    double sum_loss = 0.0, sum_kl = 0.0, sum_clip = 0.0;
+    int n = 0, k = 0;  // chunks and rows done
+    for (int row = blockIdx.x; ok && row < M; row += gridDim.x) {
+      const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.ldl;
+      T* dz = static_cast<T*>(a.dlogits) + (size_t)row * a.lddl;
+      const int y = a.targets[row];
+      if (!valid(y, V)) {
+        if (tid == 0) {
+          a.out_logp[row] = 0.f;
+          if (y != -1) atomicOr(a.status, kStatusData);
+        }
+        if (grad) zero_row(dz, V, tid, kWork);
+        continue;
+      }
+      float zy = 0.f, adv = 0.f, old = 0.f, ref = 0.f;
+      if (tid == 0) {  // on their way while the row is summed
+        zy = Act<T>::ld(z + y);
+        adv = a.advantages[a.adv_per_token ? row : row / a.T];
+        if (a.old_logp != nullptr) old = a.old_logp[row];
+        if (a.ref_logp != nullptr) ref = a.ref_logp[row];
+      }
+      const int head = head_of(z, V), nq = (V - head) / N, tail = head + nq * N, C = (nq + kVec - 1) / kVec;
+      const int again = grad && C > NS ? C - NS : 0;
+      // the element at either end that this thread has, if any
+      const int edge = tid < head ? tid : (tid >= 32 && tail + tid - 32 < V ? tail + tid - 32 : -1);
+      Online o;
+      float ze = 0.f;
+      if (edge >= 0) {
+        ze = Act<T>::ld(z + edge);
+        o.add1(ze);
+      }
+      auto wait_full = [&](int i) -> bool { return !abort_flag && ptx::mbar_wait(full(i), (uint32_t)(i / NS) & 1u, a.status); };
+      auto release = [&](int i) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty(i));
+      };
+      for (int c = 0; c < C; ++c) {
+        if (!wait_full(n + c)) {
+          ok = false;
+          break;
+        }
+        const T* src = reinterpret_cast<const T*>(ring + ((n + c) % NS) * kChunk);
+#pragma unroll
+        for (int j = 0; j < kVec / kWork; ++j) {
+          const int i = tid + j * kWork;
+          if (c * kVec + i < nq) {
+            float f[N];
+            Quad<T>::ld(src + i * N, f);
+            o.add(f);
+          }
+        }
+        if (c < again || !grad) release(n + c);
+      }
+      if (!ok) break;
+      const float wm = warp_max(o.m);
+      const double ws = warp_sum_d((double)(o.s * exp_diff(o.m, wm)));
+      if (lane == 0) {
+        s_m[k & 1][warp] = wm;
+        s_s[k & 1][warp] = ws;
+        ptx::mbar_arrive(red);
+      }
+      // warp 0 joins the 16 sums and works out the row's terms
+      if (warp == 0) {
+        if (abort_flag || !ptx::mbar_wait(red, (uint32_t)(k + 1) & 1u, a.status)) {
+          ok = false;
+          break;
+        }
+        const bool mine = lane < kWork / 32;
+        const float m0 = mine ? s_m[k & 1][lane] : -FLT_MAX, m = warp_max(m0);
+        const double S = warp_sum_d(mine ? s_s[k & 1][lane] * (double)exp_diff(m0, m) : 0.0);
+        if (lane == 0) {
+          const Row t = row_terms(a, zy, m, S, adv, old, ref, count, s_tokens[k % kMeta]);
+          s_row[k & 1] = t;
+          s_top[k & 1] = m;
+          ptx::mbar_arrive(ready);
+          a.out_logp[row] = (float)t.lp;
+          sum_loss += t.loss;
+          sum_kl += t.kl;
+          sum_clip += t.clipped;
+        }
+      }
+      if (abort_flag || !ptx::mbar_wait(ready, (uint32_t)k & 1u, a.status)) {
+        ok = false;
+        break;
+      }
+      Row t;
+      t.coef = s_row[k & 1].coef;
+      t.gz = s_row[k & 1].gz;
+      const float top = s_top[k & 1];
+      if (grad) {
+        const bool alike = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+        for (int i = again; i < C + again; ++i) {
+          const int c = i < C ? i : i - C;  // chunks again .. C - 1, then 0 .. again - 1
+          if (i >= C && !wait_full(n + i)) {
+            ok = false;
+            break;
+          }
+          const T* src = reinterpret_cast<const T*>(ring + ((n + i) % NS) * kChunk);
+#pragma unroll
+          for (int j = 0; j < kVec / kWork; ++j) {
+            const int q = c * kVec + tid + j * kWork, v0 = head + q * N;
+            if (q < nq) {
+              float f[N];
+              Quad<T>::ld(src + (tid + j * kWork) * N, f);
+              grad_quad<T>(f, v0, y, t, top);
+              if (alike) {
+                Quad<T>::st(dz + v0, f);
+              } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) Act<T>::st(dz + v0 + e, f[e]);
+              }
+            }
+          }
+          release(n + i);
+        }
+        if (edge >= 0) Act<T>::st(dz + edge, t.coef * exp_diff(ze, top) + (edge == y ? t.gz : 0.f));
+      }
+      n += C + again;
+      ++k;
+    }
+    if (!ok) abort_flag = 1;
+    if (tid == 0) {
+      part[3 * blockIdx.x] = sum_loss;
+      part[3 * blockIdx.x + 1] = sum_kl;
+      part[3 * blockIdx.x + 2] = sum_clip;
+    }
   }
 }
 
@@ -261,16 +549,40 @@ __global__ void __launch_bounds__(96) k_policy_stats(const double* part, int n, 
 
 }  // namespace
 
-void launch_policy_loss(const PolicyArgs& a, int act_bf16, double* part, int num_sms, cudaStream_t st) {
+template <typename T, int THREADS>
+static int run_rows(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
   const int M = a.B * a.T;
-  int grid = num_sms * kCtasPerSm < kPolicyMaxCtas ? num_sms * kCtasPerSm : kPolicyMaxCtas;
+  int grid = num_sms * (1024 / THREADS) < kPolicyMaxCtas ? num_sms * (1024 / THREADS) : kPolicyMaxCtas;
   if (grid > M) grid = M;
+  launch_pdl(k_policy_loss<T, THREADS>, dim3(grid), dim3(THREADS), 0, st, 1, a, part);
+  return grid;
+}
+
+template <typename T, int CPS>
+static int run_ring(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
+  const int M = a.B * a.T, grid = num_sms * CPS < M ? num_sms * CPS : M;
+  if (!smem_optin(k_policy_ring<T, CPS>, Ring<CPS>::SMEM)) return 0;
+  launch_pdl(k_policy_ring<T, CPS>, dim3(grid), dim3(kWork + 32), Ring<CPS>::SMEM, st, 1, a, part);
+  return grid;
+}
+
+template <typename T>
+static int run(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
+  const size_t bytes = (size_t)a.V * sizeof(T);
+  if (bytes <= 32768) return run_rows<T, 256>(a, part, num_sms, st);
+  return bytes <= 98304 ? run_ring<T, 2>(a, part, num_sms, st) : run_ring<T, 1>(a, part, num_sms, st);
+}
+
+bool launch_policy_loss(const PolicyArgs& a, int act_bf16, double* part, int num_sms, cudaStream_t st) {
+  int grid;
   {
     LaunchScope scope_(KK_POLICY_LOSS, st);
-    launch_pdl(act_bf16 ? k_policy_loss<bf16> : k_policy_loss<float>, dim3(grid), dim3(kThreads), 0, st, 1, a, part);
+    grid = act_bf16 ? run<bf16>(a, part, num_sms, st) : run<float>(a, part, num_sms, st);
   }
+  if (grid == 0) return false;
   LaunchScope scope_(KK_POLICY_LOSS, st);
   launch_pdl(k_policy_stats, dim3(1), dim3(96), 0, st, 1, part, grid, a.out_stats);
+  return true;
 }
 
 }  // namespace nc

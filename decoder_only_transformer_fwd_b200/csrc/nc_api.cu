@@ -1018,7 +1018,10 @@ int nc_policy_loss(const void* logits, long long ldl, const int32_t* targets, co
   a.log_low = log(a.ratio_low), a.log_high = log(a.ratio_high);
   a.kl_beta = kl_beta, a.out_stats = out_stats, a.out_logp = out_logp, a.dlogits = out_dlogits_opt, a.lddl = lddl;
   a.status = d.status;
-  launch_policy_loss(a, dtype == NC_BF16, static_cast<double*>(workspace), d.num_sms, static_cast<cudaStream_t>(stream));
+  if (!launch_policy_loss(a, dtype == NC_BF16, static_cast<double*>(workspace), d.num_sms, static_cast<cudaStream_t>(stream))) {
+    check_launch("nc_policy_loss");
+    return NC_ERR_CUDA;
+  }
   return check_launch("nc_policy_loss");
 }
 

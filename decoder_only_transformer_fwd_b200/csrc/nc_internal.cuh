@@ -265,7 +265,7 @@ struct PolicyArgs {
   long long lddl;
   int* status;
 };
-void launch_policy_loss(const PolicyArgs& a, int act_bf16, double* part, int num_sms, cudaStream_t st);
+bool launch_policy_loss(const PolicyArgs& a, int act_bf16, double* part, int num_sms, cudaStream_t st);
 
 // Raise `kernel`'s dynamic shared-memory limit to `bytes` on the current
 // device.  The attribute belongs to the device's context, so it is set per

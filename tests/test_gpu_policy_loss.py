@@ -91,6 +91,11 @@ def _check(got, want, dtype):
     (1, 5, 32768, "fp32", 0, 0.05, False),
     (1, 3, 40009, "fp32", 1, 0.05, False),
     (1, 3, 40009, "bf16", 0, 0.05, False),
+    (2, 2, 8193, "fp32", 0, 0.05, True),                     # the first sizes beyond 32 KB a row
+    (2, 2, 16391, "bf16", 1, 0.05, True),
+    (1, 3, 60001, "fp32", 0, 0.05, False),                   # a row longer than shared memory
+    (3, 150, 9001, "fp32", 1, 0.0, False),                   # several long rows per CTA
+    (3, 150, 20011, "bf16", 1, 0.05, True),
     (2, 600, 17, "fp32", 1, 0.05, True),                     # more tokens than threads
 ])
 def test_against_the_definition(B, T, V, dtype, norm, beta, per_token):
@@ -120,8 +125,16 @@ def test_strided_rows_and_odd_starts(dtype, ldl, lddl, shift):
     _check(got, PL.policy_loss(z, y, adv[:, 0], old, ref, float(np.float32(0.2)), float(np.float32(0.28)), 0.05, 0), dtype)
 
 
-def test_loss_alone_equals_the_loss_with_gradient():
-    z, y, old, ref, adv = _case(3, 3, 8, 700, "fp32")
+@pytest.mark.parametrize("dtype,V,ldl,lddl,shift", [("fp32", 9001, 9002, 9003, 1), ("bf16", 20011, 20013, 20016, 5)])
+def test_strided_long_rows(dtype, V, ldl, lddl, shift):
+    z, y, old, ref, adv = _case(10, 2, 3, V, dtype)
+    got = _run(z, y, adv[:, 0], old, ref, dtype, 0.2, 0.28, 0.05, 0, ldl, lddl, shift=shift)
+    _check(got, PL.policy_loss(z, y, adv[:, 0], old, ref, float(np.float32(0.2)), float(np.float32(0.28)), 0.05, 0), dtype)
+
+
+@pytest.mark.parametrize("V", [700, 9001, 60001])
+def test_loss_alone_equals_the_loss_with_gradient(V):
+    z, y, old, ref, adv = _case(3, 3, 8, V, "fp32")
     a = _run(z, y, adv, old, ref, "fp32", 0.2, 0.28, 0.05, 1)
     b = _run(z, y, adv, old, ref, "fp32", 0.2, 0.28, 0.05, 1, grad=False)
     assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
@@ -129,10 +142,11 @@ def test_loss_alone_equals_the_loss_with_gradient():
 
 def test_gradient_in_the_place_of_the_logits():
     import torch
-    for dtype, td in (("fp32", torch.float32), ("bf16", torch.bfloat16)):
-        z, y, old, _, adv = _case(4, 2, 40, 1003, dtype)
+    for dtype, td, V in (("fp32", torch.float32, 1003), ("bf16", torch.bfloat16, 1003), ("fp32", torch.float32, 9001),
+                         ("fp32", torch.float32, 60001)):
+        z, y, old, _, adv = _case(4, 2, 40 if V < 2000 else 4, V, dtype)
         want = _run(z, y, adv, old, None, dtype, 0.2, 0.28, 0.0, 0)
-        zd, stats, logp = _t(z, td), torch.empty(3, device="cuda"), torch.empty(2, 40, device="cuda")
+        zd, stats, logp = _t(z, td), torch.empty(3, device="cuda"), torch.empty(y.shape, device="cuda")
         nc.nc_policy_loss(zd, _t(y), _t(adv), stats, logp, zd, old_logp=_t(old), clip_low=0.2, clip_high=0.28)
         torch.cuda.synchronize()
         assert np.array_equal(zd.double().cpu().numpy(), want[2]) and np.array_equal(stats.double().cpu().numpy(), want[0])
