@@ -100,37 +100,75 @@ __device__ __forceinline__ float exp_excess(float d) {
   return s * d * d;
 }
 
+// log of a sum S >= 1 in fp64, from a table in shared memory (Tang's method:
+// "Table-driven implementation of the logarithm function", 1990): S = 2^k m,
+// c = 1 + i/128 next to m in [1, 2), log S = k log 2 + log c + log(1 + r) with
+// r = m / c - 1, |r| <= 2^-8, and six terms of the series (the next one is
+// below 2^-58); S = 1 gives 0.  The library's log takes 0.4 us on the critical
+// path of a row.
+constexpr int kLogTable = 129;
+__device__ __forceinline__ void fill_log_table(double2* tab, int tid, int threads) {
+  for (int i = tid; i < kLogTable; i += threads) {
+    const double inv = 1.0 / (1.0 + i / 128.0);
+    tab[i] = make_double2(inv, -log(inv));
+  }
+}
+__device__ __forceinline__ double log_sum(double S, const double2* tab) {
+  const int hi = __double2hiint(S), k = (hi >> 20) - 1023;
+  if ((unsigned)k > 1000u) return log(S);  // 0, infinity, NaN
+  const double m = __hiloint2double((hi & 0xfffff) | 0x3ff00000, __double2loint(S));
+  const double2 c = tab[((hi & 0xfffff) + 0x1000) >> 13];
+  const double r = fma(m, c.x, -1.0), r2 = r * r;
+  const double p = fma(r2, fma(r2, fma(r, -1.0 / 6, 0.2), fma(r, -0.25, 1.0 / 3)), fma(r, -0.5, 1.0));
+  return fma((double)k, 0.6931471805599453, c.y) + r * p;
+}
+
 // what a token's row leaves: dL/dz_v = coef e^{z_v - top} + gz [v = y]
 struct Row {
   float coef, gz;
-  double lp, loss, kl, clipped;  // the last three weighted
+};
+struct RowStats {  // the last three weighted
+  double lp, loss, kl, clipped;
 };
 
-// From the row's maximum m and sum S of e^{z - m}.  count: tokens (norm 0) or
-// sequences with a target; tokens: those of the token's sequence.
-__device__ __forceinline__ Row row_terms(const PolicyArgs& a, float zy, float m, double S, float adv, float old, float ref,
-                                         int count, int tokens) {
-  Row t;
-  t.lp = (double)zy - (double)m - log(S);
-  const double w = a.norm == 0 ? 1.0 / count : 1.0 / ((double)count * tokens);
-  const double A = (double)adv, x = a.old_logp != nullptr ? t.lp - (double)old : 0.0;
-  const bool cut = (A > 0.0 && x > a.log_high) || (A < 0.0 && x < a.log_low);
-  // with the branch decided, fp32 does: the exponents are differences
-  const double r = (double)expf((float)x);
-  double loss = -(cut ? (A > 0.0 ? a.ratio_high : a.ratio_low) : r) * A, slope = cut ? 0.0 : -r * A, kl = 0.0;
-  if (a.ref_logp != nullptr) {
-    const float d = (float)((double)ref - t.lp);
-    kl = (double)exp_excess(d);
-    loss += (double)a.kl_beta * kl;
-    slope -= (double)a.kl_beta * (kl + (double)d);
+// The part of a row's terms that its gradient waits for, from its maximum m and
+// sum S of e^{z - m}; w: the token's weight.  One thread per row runs this while
+// the others wait: fp64 only where the result needs it (lp and the comparison
+// with the borders).
+struct Terms {
+  double lp, A, w;
+  float r, d, kl;
+  bool cut;
+  __device__ __forceinline__ Row begin(const PolicyArgs& a, float zy, float m, double S, const double2* tab, float adv,
+                                       float old, float ref, double weight) {
+    lp = ((double)zy - (double)m) - log_sum(S, tab);
+    w = weight;
+    A = (double)adv;
+    const double x = a.old_logp != nullptr ? lp - (double)old : 0.0;
+    cut = (A > 0.0 && x > a.log_high) || (A < 0.0 && x < a.log_low);
+    // with the branch decided, fp32 does: the exponents are differences
+    r = expf((float)x);
+    float slope = cut ? 0.f : -r * adv;
+    kl = d = 0.f;
+    if (a.ref_logp != nullptr) {
+      d = (float)((double)ref - lp);
+      kl = exp_excess(d);
+      slope -= a.kl_beta * (kl + d);
+    }
+    Row t;
+    t.gz = (float)w * slope;
+    t.coef = -t.gz * (1.0f / (float)S);
+    return t;
   }
-  t.loss = w * loss;
-  t.kl = w * kl;
-  t.clipped = cut ? w : 0.0;
-  t.gz = (float)(w * slope);
-  t.coef = (float)(-(w * slope) / S);
-  return t;
-}
+  __device__ __forceinline__ RowStats finish(const PolicyArgs& a) const {
+    RowStats t;
+    t.lp = lp;
+    t.loss = w * (-(cut ? (A > 0.0 ? a.ratio_high : a.ratio_low) : (double)r) * A + (double)a.kl_beta * (double)kl);
+    t.kl = w * (double)kl;
+    t.clipped = cut ? w : 0.0;
+    return t;
+  }
+};
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -152,19 +190,39 @@ struct Online {
     s = s * exp_diff(m, t) + exp_diff(f, t);
     m = t;
   }
-  template <int N>
-  __device__ __forceinline__ void add(const float (&f)[N]) {
-    float t = m;
+  // K words of N elements, with one step of the maximum
+  template <int K, int N>
+  __device__ __forceinline__ void add_all(const float (&f)[K][N]) {
+    float t[K];
 #pragma unroll
-    for (int i = 0; i < N; i += 2) t = max3(t, f[i], f[i + 1]);
-    const float2 nt = make_float2(-t, -t);
-    float2 e = make_float2(s * exp_diff(m, t), 0.f);
+    for (int j = 0; j < K; ++j) {
+      t[j] = fmaxf(f[j][0], f[j][1]);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) e = __fadd2_rn(e, exp_pair(make_float2(f[i], f[i + 1]), nt));
-    s = e.x + e.y;
-    m = t;
+      for (int i = 2; i < N; i += 2) t[j] = max3(t[j], f[j][i], f[j][i + 1]);
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < K; ++j) top = fmaxf(top, t[j]);
+    const float2 nt = make_float2(-top, -top);
+    float2 e[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      e[j] = exp_pair(make_float2(f[j][0], f[j][1]), nt);
+#pragma unroll
+      for (int i = 2; i < N; i += 2) e[j] = __fadd2_rn(e[j], exp_pair(make_float2(f[j][i], f[j][i + 1]), nt));
+    }
+    s *= exp_diff(m, top);
+#pragma unroll
+    for (int j = 0; j < K; ++j) s += e[j].x + e[j].y;
+    m = top;
   }
 };
+
+// a token's weight, from the count of tokens (norm 0) or of sequences and the
+// tokens of its own (norm 1)
+__device__ __forceinline__ double weight_of(const PolicyArgs& a, int count, int tokens) {
+  return a.norm == 0 ? 1.0 / count : 1.0 / ((double)count * tokens);
+}
 
 __device__ __forceinline__ bool valid(int y, int V) { return (unsigned)y < (unsigned)V; }
 
@@ -220,7 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const
   __shared__ Row s_row;
   __shared__ float s_top;
   __shared__ int s_count;
+  __shared__ double2 s_log[kLogTable];
   pdl_launch_dependents();
+  fill_log_table(s_log, threadIdx.x, kThreads);
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int M = a.B * a.T, V = a.V;
@@ -255,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const
     if (tail + tid < V) o.add1(Act<T>::ld(z + tail + tid));
 #pragma unroll 4
     for (int i = tid; i < nq; i += kThreads) {
-      float f[Quad<T>::N];
-      Quad<T>::ld(z + head + (size_t)i * Quad<T>::N, f);
-      o.add(f);
+      float f[1][Quad<T>::N];
+      Quad<T>::ld(z + head + (size_t)i * Quad<T>::N, f[0]);
+      o.add_all(f);
     }
     const float wm = warp_max(o.m);
     const double ws = warp_sum_d((double)(o.s * exp_diff(o.m, wm)));
@@ -271,15 +331,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const
       const float m0 = mine ? s_m[lane] : -FLT_MAX, m = warp_max(m0);
       const double S = warp_sum_d(mine ? s_s[lane] * (double)exp_diff(m0, m) : 0.0);
       if (lane == 0) {
-        const Row t = row_terms(a, Act<T>::ld(z + y), m, S, a.advantages[a.adv_per_token ? row : row / a.T],
-                                a.old_logp != nullptr ? a.old_logp[row] : 0.f,
-                                a.ref_logp != nullptr ? a.ref_logp[row] : 0.f, count, tokens);
+        Terms terms;
+        s_row = terms.begin(a, Act<T>::ld(z + y), m, S, s_log, a.advantages[a.adv_per_token ? row : row / a.T],
+                            a.old_logp != nullptr ? a.old_logp[row] : 0.f, a.ref_logp != nullptr ? a.ref_logp[row] : 0.f,
+                            weight_of(a, count, tokens));
+        s_top = m;
+        const RowStats t = terms.finish(a);
         a.out_logp[row] = (float)t.lp;
         sum_loss += t.loss;
         sum_kl += t.kl;
         sum_clip += t.clipped;
-        s_row = t;
-        s_top = m;
       }
     }
     __syncthreads();
@@ -317,29 +378,30 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const
   }
 }
 
-// Long rows.  Warps 0..15 work, warp 16 copies: a row's 16-byte words (up to 15
+// Long rows.  All warps but the last work, the last one copies: a row's 16-byte words (up to 15
 // bytes at either end are read directly) in chunks of 16 KB, chunk n of the
 // CTA's sequence in slot n % NS.  Pass 1 leaves the row's last NS chunks where
 // they are; pass 2 takes those first and frees them, and then the ones before,
 // which were freed at once and are copied again (from L2).
-constexpr int kChunk = 16384, kWork = 512, kMeta = 16;
+constexpr int kChunk = 16384, kMeta = 16;
 template <int CPS> struct Ring {
-  static constexpr int NS = CPS == 1 ? 13 : 6;
+  static constexpr int NS = CPS == 1 ? 13 : 6, WORK = CPS == 1 ? 512 : 256;  // slots, working threads
   static constexpr int SMEM = NS * kChunk + 1024;
 };
 
 template <typename T, int CPS>
-__global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArgs a, double* part) {
-  constexpr int NS = Ring<CPS>::NS, N = Quad<T>::N, kVec = kChunk / 16;
+__global__ void __launch_bounds__(Ring<CPS>::WORK + 32, CPS) k_policy_ring(const PolicyArgs a, double* part) {
+  constexpr int kWork = Ring<CPS>::WORK, kWarps = kWork / 32, NS = Ring<CPS>::NS, N = Quad<T>::N, kVec = kChunk / 16, kWords = kVec / kWork;
   static_assert(NS <= kMeta, "a row has a chunk at least, so the copies run less than kMeta rows ahead");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   __shared__ uint64_t bars[2 * NS + 2];
   __shared__ Row s_row[2];
   __shared__ float s_top[2];
-  __shared__ int s_tokens[kMeta];
-  __shared__ float s_m[2][kWork / 32];
-  __shared__ double s_s[2][kWork / 32];
+  __shared__ double s_part[kMeta];  // norm 1: 1 / tokens of the sequence of the CTA's k-th row, at k % kMeta
+  __shared__ double2 s_log[kLogTable];
+  __shared__ float s_m[2][kWarps];
+  __shared__ double s_s[2][kWarps];
   __shared__ int s_count;
   __shared__ volatile int abort_flag;
   const uint32_t bar0 = ptx::smem_u32(bars);
@@ -349,12 +411,13 @@ __global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArg
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int M = a.B * a.T, V = a.V;
   pdl_launch_dependents();
+  fill_log_table(s_log, tid, kWork + 32);
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(full(s), 1);
-      ptx::mbar_init(empty(s), kWork / 32);
+      ptx::mbar_init(empty(s), kWarps);
     }
-    ptx::mbar_init(red, kWork / 32);
+    ptx::mbar_init(red, kWarps);
     ptx::mbar_init(ready, 1);
     s_count = 0;
     abort_flag = 0;
@@ -364,32 +427,39 @@ __global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArg
   __syncthreads();
   pdl_wait();
   const bool grad = a.dlogits != nullptr;
-  if (warp == kWork / 32) {
-    int n = 0, last_b = -1, tokens = 0, k = 0;
+  if (warp == kWarps) {
+    int n = 0, last_b = -1, k = 0;
+    double part_of = 1.0;
     bool ok = true;
+    int y = blockIdx.x < M ? a.targets[blockIdx.x] : -1;
     for (int row = blockIdx.x; ok && row < M; row += gridDim.x) {
-      if (!valid(a.targets[row], V)) continue;
-      if (a.norm == 1 && row / a.T != last_b) {
-        last_b = row / a.T;
-        int mine = 0;
-        for (int t = lane; t < a.T; t += 32) mine += valid(a.targets[(size_t)last_b * a.T + t], V);
-        tokens = __reduce_add_sync(0xffffffffu, mine);
-      }
+      const int y_row = y;
+      if (row + (int)gridDim.x < M) y = a.targets[row + gridDim.x];
+      if (!valid(y_row, V)) continue;
       const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.ldl;
       const int head = head_of(z, V), nq = (V - head) / N, C = (nq + kVec - 1) / kVec;
       const int again = grad && C > NS ? C - NS : 0;
+      auto copy = [&](int i) {  // the row's i-th chunk in the order of use; lane 0
+        const int c = i < C ? i : i - C;
+        const uint32_t bytes = (uint32_t)min(kVec, nq - c * kVec) * 16u;
+        if (abort_flag || !ptx::mbar_wait(empty(n), ((uint32_t)(n / NS) & 1u) ^ 1u, a.status)) return false;
+        ptx::mbar_arrive_expect_tx(full(n), bytes);
+        ptx::bulk_load(ptx::smem_u32(ring + (n % NS) * kChunk), z + head + (size_t)c * kVec * N, bytes, full(n));
+        ++n;
+        return true;
+      };
+      // the sequence's share per token is there with the row's last chunk
+      if (lane == 0 && C > 1) ok = copy(0);
+      if (a.norm == 1 && row / a.T != last_b) {
+        last_b = row / a.T;
+        int mine = 0;
+#pragma unroll 4
+        for (int t = lane; t < a.T; t += 32) mine += valid(a.targets[(size_t)last_b * a.T + t], V);
+        part_of = 1.0 / __reduce_add_sync(0xffffffffu, mine);
+      }
       if (lane == 0) {
-        s_tokens[k % kMeta] = tokens;
-        for (int i = 0; i < C + again; ++i, ++n) {
-          const int c = i < C ? i : i - C;
-          const uint32_t bytes = (uint32_t)min(kVec, nq - c * kVec) * 16u;
-          if (abort_flag || !ptx::mbar_wait(empty(n), ((uint32_t)(n / NS) & 1u) ^ 1u, a.status)) {
-            ok = false;
-            break;
-          }
-          ptx::mbar_arrive_expect_tx(full(n), bytes);
-          ptx::bulk_load(ptx::smem_u32(ring + (n % NS) * kChunk), z + head + (size_t)c * kVec * N, bytes, full(n));
-        }
+        s_part[k % kMeta] = part_of;
+        for (int i = C > 1; ok && i < C + again; ++i) ok = copy(i);
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       ++k;
@@ -409,10 +479,13 @@ __global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArg
     const int count = *(volatile int*)&s_count;
     double sum_loss = 0.0, sum_kl = 0.0, sum_clip = 0.0;
     int n = 0, k = 0;  // chunks and rows done
+    int y_next = blockIdx.x < M ? a.targets[blockIdx.x] : -1;
+    const double w_all = count > 0 ? 1.0 / count : 0.0;
     for (int row = blockIdx.x; ok && row < M; row += gridDim.x) {
       const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.ldl;
       T* dz = static_cast<T*>(a.dlogits) + (size_t)row * a.lddl;
-      const int y = a.targets[row];
+      const int y = y_next;
+      if (row + (int)gridDim.x < M) y_next = a.targets[row + gridDim.x];  // on its way during this row
       if (!valid(y, V)) {
         if (tid == 0) {
           a.out_logp[row] = 0.f;
@@ -421,9 +494,10 @@ __global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArg
         if (grad) zero_row(dz, V, tid, kWork);
         continue;
       }
-      float zy = 0.f, adv = 0.f, old = 0.f, ref = 0.f;
+      T zy = T(0.f);
+      float adv = 0.f, old = 0.f, ref = 0.f;
       if (tid == 0) {  // on their way while the row is summed
-        zy = Act<T>::ld(z + y);
+        zy = z[y];
         adv = a.advantages[a.adv_per_token ? row : row / a.T];
         if (a.old_logp != nullptr) old = a.old_logp[row];
         if (a.ref_logp != nullptr) ref = a.ref_logp[row];
@@ -449,13 +523,20 @@ __global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArg
           break;
         }
         const T* src = reinterpret_cast<const T*>(ring + ((n + c) % NS) * kChunk);
+        if ((c + 1) * kVec <= nq) {  // one maximum for all of the thread's words
+          float f[kWords][N];
 #pragma unroll
-        for (int j = 0; j < kVec / kWork; ++j) {
-          const int i = tid + j * kWork;
-          if (c * kVec + i < nq) {
-            float f[N];
-            Quad<T>::ld(src + i * N, f);
-            o.add(f);
+          for (int j = 0; j < kWords; ++j) Quad<T>::ld(src + (tid + j * kWork) * N, f[j]);
+          o.add_all(f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) {
+            const int i = tid + j * kWork;
+            if (c * kVec + i < nq) {
+              float f[1][N];
+              Quad<T>::ld(src + i * N, f[0]);
+              o.add_all(f);
+            }
           }
         }
         if (c < again || !grad) release(n + c);
@@ -468,20 +549,25 @@ __global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArg
         s_s[k & 1][warp] = ws;
         ptx::mbar_arrive(red);
       }
-      // warp 0 joins the 16 sums and works out the row's terms
+      // warp 0 joins the warps' sums and works out the row's terms
       if (warp == 0) {
         if (abort_flag || !ptx::mbar_wait(red, (uint32_t)(k + 1) & 1u, a.status)) {
           ok = false;
           break;
         }
-        const bool mine = lane < kWork / 32;
-        const float m0 = mine ? s_m[k & 1][lane] : -FLT_MAX, m = warp_max(m0);
-        const double S = warp_sum_d(mine ? s_s[k & 1][lane] * (double)exp_diff(m0, m) : 0.0);
+        const float m0 = s_m[k & 1][lane % kWarps];  // every kWarps lanes hold the same
+        float m = m0;
+#pragma unroll
+        for (int x = kWarps / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        double S = s_s[k & 1][lane % kWarps] * (double)exp_diff(m0, m);
+#pragma unroll
+        for (int x = kWarps / 2; x > 0; x >>= 1) S += __shfl_xor_sync(0xffffffffu, S, x);
         if (lane == 0) {
-          const Row t = row_terms(a, zy, m, S, adv, old, ref, count, s_tokens[k % kMeta]);
-          s_row[k & 1] = t;
+          Terms terms;
+          s_row[k & 1] = terms.begin(a, (float)zy, m, S, s_log, adv, old, ref, a.norm == 0 ? w_all : w_all * s_part[k % kMeta]);
           s_top[k & 1] = m;
           ptx::mbar_arrive(ready);
+          const RowStats t = terms.finish(a);
           a.out_logp[row] = (float)t.lp;
           sum_loss += t.loss;
           sum_kl += t.kl;
@@ -492,9 +578,7 @@ __global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArg
         ok = false;
         break;
       }
-      Row t;
-      t.coef = s_row[k & 1].coef;
-      t.gz = s_row[k & 1].gz;
+      const Row t = s_row[k & 1];
       const float top = s_top[k & 1];
       if (grad) {
         const bool alike = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
@@ -506,7 +590,7 @@ __global__ void __launch_bounds__(kWork + 32, CPS) k_policy_ring(const PolicyArg
           }
           const T* src = reinterpret_cast<const T*>(ring + ((n + i) % NS) * kChunk);
 #pragma unroll
-          for (int j = 0; j < kVec / kWork; ++j) {
+          for (int j = 0; j < kWords; ++j) {
             const int q = c * kVec + tid + j * kWork, v0 = head + q * N;
             if (q < nq) {
               float f[N];
@@ -562,7 +646,7 @@ template <typename T, int CPS>
 static int run_ring(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
   const int M = a.B * a.T, grid = num_sms * CPS < M ? num_sms * CPS : M;
   if (!smem_optin(k_policy_ring<T, CPS>, Ring<CPS>::SMEM)) return 0;
-  launch_pdl(k_policy_ring<T, CPS>, dim3(grid), dim3(kWork + 32), Ring<CPS>::SMEM, st, 1, a, part);
+  launch_pdl(k_policy_ring<T, CPS>, dim3(grid), dim3(Ring<CPS>::WORK + 32), Ring<CPS>::SMEM, st, 1, a, part);
   return grid;
 }
 
@@ -570,7 +654,7 @@ template <typename T>
 static int run(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
   const size_t bytes = (size_t)a.V * sizeof(T);
   if (bytes <= 32768) return run_rows<T, 256>(a, part, num_sms, st);
-  return bytes <= 98304 ? run_ring<T, 2>(a, part, num_sms, st) : run_ring<T, 1>(a, part, num_sms, st);
+  return bytes <= 147456 ? run_ring<T, 2>(a, part, num_sms, st) : run_ring<T, 1>(a, part, num_sms, st);
 }
 
 bool launch_policy_loss(const PolicyArgs& a, int act_bf16, double* part, int num_sms, cudaStream_t st) {
