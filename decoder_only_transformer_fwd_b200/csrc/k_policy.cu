@@ -14,11 +14,12 @@
 // whole gradient row.
 //
 // HBM bound: the logits in once, the gradient out once (2 V elements per
-// token).  Two forms, by a row's bytes:
-//   k_policy_loss  rows up to 32 KB: a CTA takes a row at a time, one pass with
-//     a running maximum and sum, then a second pass that reads the row again
-//     (from L2, where the first pass left it) and writes the gradient.  Several
-//     CTAs per SM cover each other's latencies.
+// token).  Three forms, by a row's bytes:
+//   k_policy_warp  rows up to 8 KB: a warp takes a row at a time;
+//   k_policy_loss  rows up to 32 KB: a CTA of 256 threads takes a row at a time.
+//     Both make one pass with a running maximum and sum, then a second one that
+//     reads the row again (from L2, where the first left it) and writes the
+//     gradient.  Several rows per SM cover each other's latencies.
 //   k_policy_ring  longer rows: bulk copies bring a row into a shared-memory
 //     ring, both passes read it there, and the next row's copies run meanwhile.
 #include <cfloat>
@@ -232,7 +233,15 @@ __device__ __forceinline__ int count_share(const PolicyArgs& a, int tid, int thr
   int n = 0;
   if (a.norm == 0) {
     const int M = a.B * a.T;
-    for (int i = tid; i < M; i += threads) n += valid(a.targets[i], a.V);
+    const int head = min(M, (int)((16 - (reinterpret_cast<uintptr_t>(a.targets) & 15)) & 15) / 4), quads = (M - head) / 4;
+    const int4* q = reinterpret_cast<const int4*>(a.targets + head);
+#pragma unroll 4
+    for (int i = tid; i < quads; i += threads) {
+      const int4 v = q[i];
+      n += valid(v.x, a.V) + valid(v.y, a.V) + valid(v.z, a.V) + valid(v.w, a.V);
+    }
+    if (tid < head) n += valid(a.targets[tid], a.V);
+    if (head + 4 * quads + tid < M && tid < 4) n += valid(a.targets[head + 4 * quads + tid], a.V);
   } else {
     const int lane = tid & 31;
     for (int b = tid >> 5; b < a.B; b += threads >> 5) {
@@ -269,6 +278,119 @@ __device__ __forceinline__ void zero_row(T* dz, int V, int tid, int threads) {
   if (tail + tid < V) Act<T>::st(dz + tail + tid, 0.f);
   float f[Quad<T>::N] = {};
   for (int i = tid; i < nq; i += threads) Quad<T>::st(dz + head + (size_t)i * Quad<T>::N, f);
+}
+
+// the second pass over a row: threads tid, tid + threads, ...
+template <typename T>
+__device__ __forceinline__ void write_grad(const T* z, T* dz, int V, int y, const Row& t, float top, int tid, int threads) {
+  // the gradient's own 16-byte boundaries; the logits at the same element
+  // offsets when both rows start alike, else one element at a time
+  const int head = head_of(dz, V);
+  const bool alike = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+  const int nq = (V - head) / Quad<T>::N, tail = head + nq * Quad<T>::N;
+  auto one = [&](int v) { Act<T>::st(dz + v, t.coef * exp_diff(Act<T>::ld(z + v), top) + (v == y ? t.gz : 0.f)); };
+  if (tid < head) one(tid);
+  if (tail + tid < V) one(tail + tid);
+#pragma unroll 4
+  for (int i = tid; i < nq; i += threads) {
+    const int v0 = head + i * Quad<T>::N;
+    float f[Quad<T>::N];
+    if (alike) {
+      Quad<T>::ld(z + v0, f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < Quad<T>::N; ++e) f[e] = Act<T>::ld(z + v0 + e);
+    }
+    grad_quad<T>(f, v0, y, t, top);
+    Quad<T>::st(dz + v0, f);
+  }
+}
+
+// the first pass: this thread's running maximum and sum
+template <typename T>
+__device__ __forceinline__ Online row_sum(const T* z, int V, int tid, int threads) {
+  const int head = head_of(z, V), nq = (V - head) / Quad<T>::N, tail = head + nq * Quad<T>::N;
+  Online o;
+  if (tid < head) o.add1(Act<T>::ld(z + tid));
+  if (tail + tid < V) o.add1(Act<T>::ld(z + tail + tid));
+#pragma unroll 4
+  for (int i = tid; i < nq; i += threads) {
+    float f[1][Quad<T>::N];
+    Quad<T>::ld(z + head + (size_t)i * Quad<T>::N, f[0]);
+    o.add_all(f);
+  }
+  return o;
+}
+
+// Short rows: a warp takes `per` consecutive rows (of one sequence, mostly, so
+// that its tokens are counted once), one after the other.
+constexpr int kWarpRows = 8, kWarpCtas = 4;  // rows at a time per CTA, CTAs per SM
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarpRows, kWarpCtas) k_policy_warp(const PolicyArgs a, double* part, int per) {
+  __shared__ double s_sum[kWarpRows][3];
+  __shared__ int s_count;
+  __shared__ double2 s_log[kLogTable];
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  fill_log_table(s_log, tid, 32 * kWarpRows);
+  if (tid == 0) s_count = 0;
+  pdl_wait();
+  __syncthreads();
+  const int share = __reduce_add_sync(0xffffffffu, count_share(a, tid, 32 * kWarpRows));
+  if (lane == 0 && share != 0) atomicAdd(&s_count, share);
+  __syncthreads();
+  const int count = s_count, M = a.B * a.T, V = a.V;
+  const double w_all = count > 0 ? 1.0 / count : 0.0;
+  double part_of = 1.0, sums[3] = {0.0, 0.0, 0.0};
+  const long long first = ((long long)blockIdx.x * kWarpRows + warp) * per;
+  const int last = (int)min(first + per, (long long)M);
+  int last_b = -1;
+  for (int row = (int)min(first, (long long)M); row < last; ++row) {
+    const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.ldl;
+    T* dz = a.dlogits != nullptr ? static_cast<T*>(a.dlogits) + (size_t)row * a.lddl : nullptr;
+    const int y = a.targets[row];
+    if (!valid(y, V)) {
+      if (lane == 0) {
+        a.out_logp[row] = 0.f;
+        if (y != -1) atomicOr(a.status, kStatusData);
+      }
+      if (dz != nullptr) zero_row(dz, V, lane, 32);
+      continue;
+    }
+    const float zy = Act<T>::ld(z + y), adv = a.advantages[a.adv_per_token ? row : row / a.T];
+    const float old = a.old_logp != nullptr ? a.old_logp[row] : 0.f, ref = a.ref_logp != nullptr ? a.ref_logp[row] : 0.f;
+    if (a.norm == 1 && row / a.T != last_b) {
+      last_b = row / a.T;
+      int mine = 0;
+#pragma unroll 4
+      for (int t = lane; t < a.T; t += 32) mine += valid(a.targets[(size_t)last_b * a.T + t], V);
+      part_of = 1.0 / __reduce_add_sync(0xffffffffu, mine);
+    }
+    const Online o = row_sum(z, V, lane, 32);
+    const float top = warp_max(o.m);
+    const double S = warp_sum_d((double)(o.s * exp_diff(o.m, top)));
+    // all lanes work the terms out alike
+    Terms terms;
+    const Row t = terms.begin(a, zy, top, S, s_log, adv, old, ref, w_all * part_of);
+    if (dz != nullptr) write_grad(z, dz, V, y, t, top, lane, 32);
+    if (lane == 0) {
+      const RowStats st = terms.finish(a);
+      a.out_logp[row] = (float)st.lp;
+      sums[0] += st.loss;
+      sums[1] += st.kl;
+      sums[2] += st.clipped;
+    }
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) s_sum[warp][i] = sums[i];
+  }
+  __syncthreads();
+  if (tid < 3) {
+    double v = 0.0;
+    for (int i = 0; i < kWarpRows; ++i) v += s_sum[i][tid];
+    part[3 * blockIdx.x + tid] = v;
+  }
 }
 
 template <typename T, int kThreads>
@@ -309,16 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const
       tokens = 0;
       for (int t0 = 0; t0 < a.T; t0 += kThreads) tokens += __syncthreads_count(t0 + tid < a.T && valid(tg[t0 + tid], V));
     }
-    const int head = head_of(z, V), nq = (V - head) / Quad<T>::N, tail = head + nq * Quad<T>::N;
-    Online o;
-    if (tid < head) o.add1(Act<T>::ld(z + tid));
-    if (tail + tid < V) o.add1(Act<T>::ld(z + tail + tid));
-#pragma unroll 4
-    for (int i = tid; i < nq; i += kThreads) {
-      float f[1][Quad<T>::N];
-      Quad<T>::ld(z + head + (size_t)i * Quad<T>::N, f[0]);
-      o.add_all(f);
-    }
+    const Online o = row_sum(z, V, tid, kThreads);
     const float wm = warp_max(o.m);
     const double ws = warp_sum_d((double)(o.s * exp_diff(o.m, wm)));
     if (lane == 0) {
@@ -346,28 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const
     __syncthreads();
     if (dz != nullptr) {
       const Row t = s_row;
-      const float top = s_top;
-      // the gradient's own 16-byte boundaries; the logits at the same element
-      // offsets when both rows start alike, else one element at a time
-      const int head = head_of(dz, V);
-      const bool alike = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-      const int nq = (V - head) / Quad<T>::N, tail = head + nq * Quad<T>::N;
-      auto one = [&](int v) { Act<T>::st(dz + v, t.coef * exp_diff(Act<T>::ld(z + v), top) + (v == y ? t.gz : 0.f)); };
-      if (tid < head) one(tid);
-      if (tail + tid < V) one(tail + tid);
-#pragma unroll 4
-      for (int i = tid; i < nq; i += kThreads) {
-        const int v0 = head + i * Quad<T>::N;
-        float f[Quad<T>::N];
-        if (alike) {
-          Quad<T>::ld(z + v0, f);
-        } else {
-#pragma unroll
-          for (int e = 0; e < Quad<T>::N; ++e) f[e] = Act<T>::ld(z + v0 + e);
-        }
-        grad_quad<T>(f, v0, y, t, top);
-        Quad<T>::st(dz + v0, f);
-      }
+      write_grad(z, dz, V, y, t, s_top, tid, kThreads);
     }
     __syncthreads();  // the next row reuses the scratch
   }
@@ -642,6 +734,16 @@ static int run_rows(const PolicyArgs& a, double* part, int num_sms, cudaStream_t
   return grid;
 }
 
+template <typename T>
+static int run_warp(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
+  const int M = a.B * a.T;
+  int grid = num_sms * kWarpCtas < kPolicyMaxCtas ? num_sms * kWarpCtas : kPolicyMaxCtas;
+  const int per = (M + grid * kWarpRows - 1) / (grid * kWarpRows);
+  grid = (M + per * kWarpRows - 1) / (per * kWarpRows);
+  launch_pdl(k_policy_warp<T>, dim3(grid), dim3(32 * kWarpRows), 0, st, 1, a, part, per);
+  return grid;
+}
+
 template <typename T, int CPS>
 static int run_ring(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
   const int M = a.B * a.T, grid = num_sms * CPS < M ? num_sms * CPS : M;
@@ -653,8 +755,18 @@ static int run_ring(const PolicyArgs& a, double* part, int num_sms, cudaStream_t
 template <typename T>
 static int run(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
   const size_t bytes = (size_t)a.V * sizeof(T);
+  const int M = a.B * a.T;
+  // measured, fp32, 16384 rows: 2048 words 96 us with a CTA of 256 threads per
+  // row, 56 us with a warp; 8192 words 191 us against 198 with 128 threads
+  if (bytes <= 8192) return run_warp<T>(a, part, num_sms, st);
   if (bytes <= 32768) return run_rows<T, 256>(a, part, num_sms, st);
-  return bytes <= 147456 ? run_ring<T, 2>(a, part, num_sms, st) : run_ring<T, 1>(a, part, num_sms, st);
+  // two CTAs per SM overlap one row's sums with the other's writes, unless much
+  // of a row does not fit half the memory and is copied twice (8192 rows: 32768
+  // words 337 us against 361 with one CTA, 60000 words of 4096 rows 375 against
+  // 310); up to a row per SM, one CTA with twice the threads has it sooner
+  // (64 rows of 32768 words: 9.9 us against 12.3)
+  if (bytes <= 147456 && M > num_sms) return run_ring<T, 2>(a, part, num_sms, st);
+  return run_ring<T, 1>(a, part, num_sms, st);
 }
 
 bool launch_policy_loss(const PolicyArgs& a, int act_bf16, double* part, int num_sms, cudaStream_t st) {

@@ -87,6 +87,10 @@ def _check(got, want, dtype):
     (3, 5, 1000, "fp32", 1, 0.05, True),
     (3, 7, 1001, "bf16", 1, 0.05, False),                    # odd rows: every alignment
     (2, 300, 513, "fp32", 0, 0.0, True),
+    (5, 1100, 40, "fp32", 1, 0.1, True),                     # two rows per warp
+    (2, 7, 2048, "fp32", 0, 0.05, False),                    # the border of 8 KB a row, and beyond
+    (2, 7, 2049, "fp32", 0, 0.05, False),
+    (3, 400, 2051, "fp32", 1, 0.05, False),                  # several rows per CTA
     (4, 90, 4099, "bf16", 0, 0.2, True),                     # more rows than CTAs
     (1, 5, 32768, "fp32", 0, 0.05, False),
     (1, 3, 40009, "fp32", 1, 0.05, False),
