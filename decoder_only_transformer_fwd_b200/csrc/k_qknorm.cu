@@ -18,7 +18,7 @@ namespace nc {
 namespace {
 
 constexpr int kD = 128, kHalf = 64;
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kMaxTok = 8;
 
 struct RopeFreq {
   // theta_i / 2 pi as a fraction of 2^64: position * turns mod 2^64 is the
@@ -140,25 +140,35 @@ struct FwdArgs {
 
 // A CTA takes `tok` tokens; its 32 eight-lane groups share them out evenly,
 // and a group walks every (32 / tok)-th head vector of its token with the
-// token's angles in registers.
+// token's angles in registers, the next vector's load under the current one's
+// arithmetic (and the first one's under the angles').
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant__ FwdArgs<T> a) {
-  __shared__ float cs[8 * 2 * kHalf];
+  __shared__ float cs[kMaxTok * 2 * kHalf];
   pdl_launch_dependents();
   pdl_wait();
   const int n0 = blockIdx.x * a.tok;
   const int ntok = min(a.tok, a.N - n0);
-  fill_angles(a.f, a.positions, n0, ntok, cs, a.status);
-  __syncthreads();
   const int group = threadIdx.x >> 3, j = threadIdx.x & 7;
   const int per = 32 / a.tok;  // groups per token
   const int tl = group / per;
-  if (tl >= ntok) return;
-  const unsigned mask = 0xffu << ((threadIdx.x & 31) & ~7);
+  const bool live = tl < ntok;
   const int n = n0 + tl;
-  long long slot = a.slots != nullptr ? (long long)a.slots[n] : (long long)n;
+  const int kept = (a.v != nullptr ? 2 : 1) * a.Hkv;
+  auto source = [&](int h) -> const T* {
+    const int hk = h - a.H, hv = hk - a.Hkv;
+    return hk < 0 ? a.q + n * a.ldq + h * kD : (hv < 0 ? a.k + n * a.ldk + hk * kD : a.v + n * a.ldv + hv * kD);
+  };
+  int h = group % per;
+  Raw<T> next;
+  if (live && h < a.H + kept) next.load(source(h), j);
+  long long slot = live ? (a.slots != nullptr ? (long long)a.slots[n] : (long long)n) : 0;
+  fill_angles(a.f, a.positions, n0, ntok, cs, a.status);
+  __syncthreads();
+  if (!live) return;
+  const unsigned mask = 0xffu << ((threadIdx.x & 31) & ~7);
   if (slot < -1 || slot >= a.out_rows) {  // -1: a token that is not kept
-    if (group % per == 0 && j == 0) atomicOr(a.status, kStatusData);
+    if (h == 0 && j == 0) atomicOr(a.status, kStatusData);
     slot = -1;
   }
   float c[8], s[8];
@@ -167,15 +177,13 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant
     c[i] = cs[tl * 2 * kHalf + 8 * j + i];
     s[i] = cs[tl * 2 * kHalf + kHalf + 8 * j + i];
   }
-  const int heads = a.H + (slot >= 0 ? (a.v != nullptr ? 2 : 1) * a.Hkv : 0);
-#pragma unroll 2
-  for (int h = group % per; h < heads; h += per) {
+  const int heads = a.H + (slot >= 0 ? kept : 0);
+  for (; h < heads; h += per) {
     const int hk = h - a.H, hv = hk - a.Hkv;
-    const T* src = hk < 0 ? a.q + n * a.ldq + h * kD : (hv < 0 ? a.k + n * a.ldk + hk * kD : a.v + n * a.ldv + hv * kD);
+    Raw<T> raw = next;
+    if (h + per < heads) next.load(source(h + per), j);
     T* dst = hk < 0 ? a.qo + n * a.ldqo + h * kD
                     : (hv < 0 ? a.ko + slot * a.ldko + hk * kD : a.vo + slot * a.ldvo + hv * kD);
-    Raw<T> raw;
-    raw.load(src, j);
     if (hv < 0) {
       Vec x = raw.get();
       float ss = 0.f;
@@ -209,33 +217,39 @@ struct BwdArgs {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope_bwd(const __grid_constant__ BwdArgs<T> a) {
-  __shared__ float cs[8 * 2 * kHalf];
+  __shared__ float cs[kMaxTok * 2 * kHalf];
   pdl_launch_dependents();
   pdl_wait();
   const int n0 = blockIdx.x * a.tok;
   const int ntok = min(a.tok, a.N - n0);
-  fill_angles(a.f, a.positions, n0, ntok, cs, a.status);
-  __syncthreads();
   const int group = threadIdx.x >> 3, j = threadIdx.x & 7;
   const int per = 32 / a.tok;
   const int tl = group / per;
-  if (tl >= ntok) return;
+  const bool live = tl < ntok;
+  const int n = n0 + tl, heads = a.H + a.Hkv;
+  int h = group % per;
+  Raw<T> nx, ng;
+  auto load = [&](int h) {
+    const int hk = h - a.H;
+    nx.load(hk < 0 ? a.q + n * a.ldq + h * kD : a.k + n * a.ldk + hk * kD, j);
+    ng.load(hk < 0 ? a.gq + n * a.ldgq + h * kD : a.gk + n * a.ldgk + hk * kD, j);
+  };
+  if (live && h < heads) load(h);
+  fill_angles(a.f, a.positions, n0, ntok, cs, a.status);
+  __syncthreads();
+  if (!live) return;
   const unsigned mask = 0xffu << ((threadIdx.x & 31) & ~7);
-  const int n = n0 + tl;
   float c[8], s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     c[i] = cs[tl * 2 * kHalf + 8 * j + i];
     s[i] = cs[tl * 2 * kHalf + kHalf + 8 * j + i];
   }
-#pragma unroll 2
-  for (int h = group % per; h < a.H + a.Hkv; h += per) {
+  for (; h < heads; h += per) {
     const int hk = h - a.H;
-    Raw<T> rx, rg;
-    rx.load(hk < 0 ? a.q + n * a.ldq + h * kD : a.k + n * a.ldk + hk * kD, j);
-    rg.load(hk < 0 ? a.gq + n * a.ldgq + h * kD : a.gk + n * a.ldgk + hk * kD, j);
-    const Vec x = rx.get();
-    Vec g = rg.get();
+    const Vec x = nx.get();
+    Vec g = ng.get();
+    if (h + per < heads) load(h + per);
     float ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -254,8 +268,9 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope_bwd(const __grid_cons
       g.a[i] = r * (g.a[i] - x.a[i] * t);
       g.b[i] = r * (g.b[i] - x.b[i] * t);
     }
-    rg.set(g);
-    rg.store(hk < 0 ? a.dq + n * a.lddq + h * kD : a.dk + n * a.lddk + hk * kD, j);
+    Raw<T> out;
+    out.set(g);
+    out.store(hk < 0 ? a.dq + n * a.lddq + h * kD : a.dk + n * a.lddk + hk * kD, j);
   }
 }
 
@@ -267,51 +282,59 @@ void rope_freq(float base, RopeFreq* f) {
   for (int i = 0; i < kHalf; ++i, t *= ratio) f->turns[i] = (unsigned long long)(t * 18446744073709551616.0L);
 }
 
-int tokens_per_cta(int N) { return N >= 4 * 1024 ? 4 : 1; }
+// Tokens per CTA: as many as leave a CTA for each SM and a third more, and a
+// group at most eight vectors.  Measured, bf16, 12 + 12 heads: forward of 300
+// tokens 3.4 us with 1 token (4.2 with 4), of 1000 tokens 6.6 us with 4 (8.2
+// with 1, 9.5 with 8); backward of 3000 tokens 10.0 us with 8 (11.0 with 4).
+int tokens_per_cta(int N, int heads, int num_sms) {
+  int tok = kMaxTok;
+  while (tok > 1 && (heads * tok > 32 * 8 || (long long)3 * ((N + tok - 1) / tok) < (long long)4 * num_sms)) tok /= 2;
+  return tok;
+}
 
 }  // namespace
 
 template <typename T>
-static void run_fwd(const QkNormArgs& p, cudaStream_t st) {
+static void run_fwd(const QkNormArgs& p, int num_sms, cudaStream_t st) {
   FwdArgs<T> a;
   a.q = static_cast<const T*>(p.q), a.k = static_cast<const T*>(p.k), a.v = static_cast<const T*>(p.v);
   a.qo = static_cast<T*>(p.q_out), a.ko = static_cast<T*>(p.k_out), a.vo = static_cast<T*>(p.v_out);
   a.ldq = p.ldq, a.ldk = p.ldk, a.ldv = p.ldv, a.ldqo = p.ldqo, a.ldko = p.ldko, a.ldvo = p.ldvo;
   a.positions = p.positions, a.slots = p.slots;
-  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.tok = tokens_per_cta(p.N);
+  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.tok = tokens_per_cta(p.N, p.H + (p.v != nullptr ? 2 : 1) * p.Hkv, num_sms);
   a.out_rows = p.out_rows, a.alpha = p.alpha, a.eps = p.eps, a.status = p.status;
   rope_freq(p.rope_base, &a.f);
   LaunchScope scope_(KK_QK_NORM_ROPE, st);
   launch_pdl(k_qk_norm_rope<T>, dim3((p.N + a.tok - 1) / a.tok), dim3(kThreads), 0, st, 1, a);
 }
 
-void launch_qk_norm_rope(const QkNormArgs& p, int act_bf16, cudaStream_t st) {
+void launch_qk_norm_rope(const QkNormArgs& p, int act_bf16, int num_sms, cudaStream_t st) {
   if (act_bf16)
-    run_fwd<bf16>(p, st);
+    run_fwd<bf16>(p, num_sms, st);
   else
-    run_fwd<float>(p, st);
+    run_fwd<float>(p, num_sms, st);
 }
 
 template <typename T>
-static void run_bwd(const QkNormArgs& p, cudaStream_t st) {
+static void run_bwd(const QkNormArgs& p, int num_sms, cudaStream_t st) {
   BwdArgs<T> a;
   a.q = static_cast<const T*>(p.q), a.k = static_cast<const T*>(p.k);
   a.gq = static_cast<const T*>(p.dq_hat), a.gk = static_cast<const T*>(p.dk_hat);
   a.dq = static_cast<T*>(p.q_out), a.dk = static_cast<T*>(p.k_out);
   a.ldq = p.ldq, a.ldk = p.ldk, a.ldgq = p.ldgq, a.ldgk = p.ldgk, a.lddq = p.ldqo, a.lddk = p.ldko;
   a.positions = p.positions;
-  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.tok = tokens_per_cta(p.N);
+  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.tok = tokens_per_cta(p.N, p.H + p.Hkv, num_sms);
   a.alpha = p.alpha, a.eps = p.eps, a.status = p.status;
   rope_freq(p.rope_base, &a.f);
   LaunchScope scope_(KK_QK_NORM_ROPE, st);
   launch_pdl(k_qk_norm_rope_bwd<T>, dim3((p.N + a.tok - 1) / a.tok), dim3(kThreads), 0, st, 1, a);
 }
 
-void launch_qk_norm_rope_bwd(const QkNormArgs& p, int act_bf16, cudaStream_t st) {
+void launch_qk_norm_rope_bwd(const QkNormArgs& p, int act_bf16, int num_sms, cudaStream_t st) {
   if (act_bf16)
-    run_bwd<bf16>(p, st);
+    run_bwd<bf16>(p, num_sms, st);
   else
-    run_bwd<float>(p, st);
+    run_bwd<float>(p, num_sms, st);
 }
 
 }  // namespace nc

@@ -896,7 +896,7 @@ int nc_qk_norm_rope(const void* q, long long ldq, const void* k, long long ldk, 
   DevInfo d;
   if (!dev_info(&d)) return NC_ERR_CUDA;
   p.status = d.status;
-  launch_qk_norm_rope(p, bf, static_cast<cudaStream_t>(stream));
+  launch_qk_norm_rope(p, bf, d.num_sms, static_cast<cudaStream_t>(stream));
   return check_launch("nc_qk_norm_rope");
 }
 
@@ -926,7 +926,7 @@ int nc_qk_norm_rope_backward(const void* q, long long ldq, const void* k, long l
   DevInfo d;
   if (!dev_info(&d)) return NC_ERR_CUDA;
   p.status = d.status;
-  launch_qk_norm_rope_bwd(p, bf, static_cast<cudaStream_t>(stream));
+  launch_qk_norm_rope_bwd(p, bf, d.num_sms, static_cast<cudaStream_t>(stream));
   return check_launch("nc_qk_norm_rope_backward");
 }
 

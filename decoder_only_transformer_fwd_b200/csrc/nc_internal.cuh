@@ -222,8 +222,8 @@ struct QkNormArgs {
   float alpha, rope_base, eps;
   int* status;
 };
-void launch_qk_norm_rope(const QkNormArgs& p, int act_bf16, cudaStream_t st);
-void launch_qk_norm_rope_bwd(const QkNormArgs& p, int act_bf16, cudaStream_t st);
+void launch_qk_norm_rope(const QkNormArgs& p, int act_bf16, int num_sms, cudaStream_t st);
+void launch_qk_norm_rope_bwd(const QkNormArgs& p, int act_bf16, int num_sms, cudaStream_t st);
 
 // Attention over a shared prefix and the rows' own keys (k_prefix_attn.cu).
 constexpr int kPrefixCtas = 296;  // two on each of 148 SMs
