@@ -125,6 +125,18 @@ __device__ __forceinline__ void fill_angles(const RopeFreq& f, const int32_t* po
   }
 }
 
+// A lane's cos and sin, read again for every vector: kept in registers they
+// would cost a CTA per SM, and with it the loads in flight that HBM needs.
+__device__ __forceinline__ void load_angles(uint32_t p, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(c[i]), "=f"(c[i + 1]), "=f"(c[i + 2]), "=f"(c[i + 3]) : "r"(p + 4 * i));
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(s[i]), "=f"(s[i + 1]), "=f"(s[i + 2]), "=f"(s[i + 3]) : "r"(p + 4 * (kHalf + i)));
+  }
+}
+
 template <typename T>
 struct FwdArgs {
   const T *q, *k, *v;
@@ -144,7 +156,7 @@ struct FwdArgs {
 // arithmetic (and the first one's under the angles').
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant__ FwdArgs<T> a) {
-  __shared__ float cs[kMaxTok * 2 * kHalf];
+  __shared__ __align__(16) float cs[kMaxTok * 2 * kHalf];
   pdl_launch_dependents();
   pdl_wait();
   const int n0 = blockIdx.x * a.tok;
@@ -171,12 +183,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant
     if (h == 0 && j == 0) atomicOr(a.status, kStatusData);
     slot = -1;
   }
-  float c[8], s[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = cs[tl * 2 * kHalf + 8 * j + i];
-    s[i] = cs[tl * 2 * kHalf + kHalf + 8 * j + i];
-  }
+  const uint32_t my_cs = static_cast<uint32_t>(__cvta_generic_to_shared(cs + tl * 2 * kHalf + 8 * j));
   const int heads = a.H + (slot >= 0 ? kept : 0);
   for (; h < heads; h += per) {
     const int hk = h - a.H, hv = hk - a.Hkv;
@@ -191,6 +198,8 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant
       for (int i = 0; i < 8; ++i) ss += x.a[i] * x.a[i] + x.b[i] * x.b[i];
       ss = sum8(ss, mask);
       const float r = a.alpha * rsqrtf(ss * (1.0f / kD) + a.eps);
+      float c[8], s[8];
+      load_angles(my_cs, c, s);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float u = x.a[i], w = x.b[i];
@@ -215,9 +224,10 @@ struct BwdArgs {
   RopeFreq f;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_qk_norm_rope_bwd(const __grid_constant__ BwdArgs<T> a) {
-  __shared__ float cs[kMaxTok * 2 * kHalf];
+// MINB: CTAs per SM that the registers are kept to.
+template <typename T, int MINB>
+__global__ void __launch_bounds__(kThreads, MINB) k_qk_norm_rope_bwd(const __grid_constant__ BwdArgs<T> a) {
+  __shared__ __align__(16) float cs[kMaxTok * 2 * kHalf];
   pdl_launch_dependents();
   pdl_wait();
   const int n0 = blockIdx.x * a.tok;
@@ -239,17 +249,14 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope_bwd(const __grid_cons
   __syncthreads();
   if (!live) return;
   const unsigned mask = 0xffu << ((threadIdx.x & 31) & ~7);
-  float c[8], s[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = cs[tl * 2 * kHalf + 8 * j + i];
-    s[i] = cs[tl * 2 * kHalf + kHalf + 8 * j + i];
-  }
+  const uint32_t my_cs = static_cast<uint32_t>(__cvta_generic_to_shared(cs + tl * 2 * kHalf + 8 * j));
   for (; h < heads; h += per) {
     const int hk = h - a.H;
     const Vec x = nx.get();
     Vec g = ng.get();
     if (h + per < heads) load(h + per);
+    float c[8], s[8];
+    load_angles(my_cs, c, s);
     float ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -327,7 +334,15 @@ static void run_bwd(const QkNormArgs& p, int num_sms, cudaStream_t st) {
   a.alpha = p.alpha, a.eps = p.eps, a.status = p.status;
   rope_freq(p.rope_base, &a.f);
   LaunchScope scope_(KK_QK_NORM_ROPE, st);
-  launch_pdl(k_qk_norm_rope_bwd<T>, dim3((p.N + a.tok - 1) / a.tok), dim3(kThreads), 0, st, 1, a);
+  const int grid = (p.N + a.tok - 1) / a.tok;
+  // bf16 moves 32 bytes per thread and load, so a long batch wants the fourth CTA
+  // on an SM (8192 tokens, 12 + 12 heads: 25.5 us against 28.2); with fewer CTAs
+  // than that the freer schedule is faster (3000 tokens: 9.8 us against 12.2)
+  auto kernel = k_qk_norm_rope_bwd<T, 3>;
+  if constexpr (sizeof(T) == 2) {
+    if (grid >= 4 * num_sms) kernel = k_qk_norm_rope_bwd<T, 4>;
+  }
+  launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, st, 1, a);
 }
 
 void launch_qk_norm_rope_bwd(const QkNormArgs& p, int act_bf16, int num_sms, cudaStream_t st) {
