@@ -66,8 +66,13 @@ constexpr uint32_t TMEM_COLS = 256;        // S0 64 | S1 64 | O 128
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.6931471805599453f;
 // What a unit costs besides its tiles (query load, set-up, rows out), in tiles.
-constexpr int kUnitCost = 1;
-constexpr int kPrefixSplitRows = 4096;
+// 1 against 2 against 3: 8 rows over 32768 keys 43.4, 39.9, 39.8 us; 64 rows over
+// 4096 keys and their own 1024 42.8, 42.8, 44.3 us.
+constexpr int kUnitCost = 2;
+// Query rows up to which a row's pieces are joined by four warps: the CTAs that
+// 148 SMs hold at once.  2048 rows: 29.3 us for the whole call against 30.5 with
+// one warp; 3600 rows: 35.5 against 31.7.
+constexpr int kPrefixSplitRows = 148 * 16;
 
 struct Piece {
   int suffix, seq, hk;  // side, group or row, key head
@@ -153,7 +158,8 @@ __device__ void fill_tables(const PrefixAttnArgs& a, int* start, int2* seen, int
     }
     if (lane == 0) start[i] = c;
   }
-  for (int i = threadIdx.x; i < a.bins_s; i += kThreads) {
+  // rows from the last thread down: few rows are not behind warp 0's groups
+  for (int i = kThreads - 1 - threadIdx.x; i < a.bins_s; i += kThreads) {
     int c = 0;
     for (int b = i * a.bin_s; b < min(a.B, (i + 1) * a.bin_s); ++b) c += a.band * suffix_cost(a, suffix_seq(a, b));
     start[a.bins_p + i] = c;
@@ -292,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                   const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
                   const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
                   const PrefixAttnArgs a) {
-  pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
@@ -310,6 +315,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // Tensor memory first: the second CTA of an SM starts only when the first has
+  // given up its allocation permit (measured: 2.6 us after it with the
+  // allocation behind the tables of starts, 0.6 us with it here).  The next
+  // kernel may start only after that, so that nothing that waits for this one
+  // holds tensor memory that it still needs.
+  if (warp == kWarpMma) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+    pdl_launch_dependents();
+  }
   if (threadIdx.x == 0) {
     ptx::mbar_init(bar(B_QF), 1);
     ptx::mbar_init(bar(B_QE), 1);
@@ -342,11 +358,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const long long v_begin = (long long)(blockIdx.x / a.bands) * share;
   const bool works = v_begin < total;
   const int v0 = (int)min(v_begin, (long long)total), v1 = (int)min(v_begin + share, (long long)total);
-  if (works && warp == kWarpMma) {
-    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
-    ptx::tmem_relinquish();
-    ptx::tc_fence_before();
-  }
+  ptx::tc_fence_after();  // the allocation, before the barriers of fill_tables
+  const uint32_t tmem = *tmem_slot;
   if (warp < 4) {  // while the first copies are on their way
     const int units_p = a.P_max > 0 ? a.G * a.Hkv * a.tiles_p : 0, units_s = a.S_max > 0 ? a.B * a.Hkv * a.tiles_s : 0;
     for (int u = blockIdx.x * 128 + threadIdx.x; u < units_p + units_s; u += a.ctas * 128)
@@ -360,11 +373,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int b = threadIdx.x; b < a.B; b += 128) bad |= (unsigned)a.suffix_lens[b] > (unsigned)a.S_max;
     if (bad) atomicOr(a.status, kStatusData);
   }
-  if (!works) return;
-  // warp 4 needs neither tensor memory nor this
-  if (warp != kWarpTma) asm volatile("bar.sync 1, 160;" ::: "memory");
-  ptx::tc_fence_after();
-  const uint32_t tmem = warp != kWarpTma ? *tmem_slot : 0u;
+  if (!works) {
+    if (warp == kWarpMma) ptx::tmem_dealloc(tmem, TMEM_COLS);
+    return;
+  }
   auto sSlot = [&](int s) { return ptx::smem_u32(smem + OFF_SLOT + s * SLOT_BYTES); };
   const uint32_t sQ = ptx::smem_u32(smem);
   const int R = a.H / a.Hkv;
@@ -708,29 +720,31 @@ __global__ void __launch_bounds__(128) k_prefix_combine(const PrefixAttnArgs a) 
   for (int p0 = w0; p0 < parts; p0 += 32 * WPR) {
     // lane i holds piece p0 + WPR i: its weight, and where its output row is
     const int p = p0 + WPR * lane, n = min(32, (parts - p0 + WPR - 1) / WPR);
-    float l = -INFINITY;
-    const float* o = a.part_op;
-    if (p < parts) {
-      const bool side = p >= in_p.y;
-      const long long r = side ? (long long)(in_s.x + p - in_p.y) * (a.box_s * R) + rs : (long long)(in_p.x + p) * (a.box_p * R) + rp;
-      l = (side ? a.part_ls : a.part_lp)[r];
-      o = (side ? a.part_os : a.part_op) + r * kD;
-    }
+    const bool side = p >= in_p.y;
+    const long long r = side ? (long long)(in_s.x + min(p, parts - 1) - in_p.y) * (a.box_s * R) + rs
+                             : (long long)(in_p.x + p) * (a.box_p * R) + rp;
+    const float* lse = (side ? a.part_ls : a.part_lp) + r;
+    const unsigned long long o = reinterpret_cast<unsigned long long>((side ? a.part_os : a.part_op) + r * kD);
+    // four rows in flight, beside the weights; a piece of weight 0 may have left
+    // no row (whatever is there is read and not used)
+    float4 x[4];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned long long oi = __shfl_sync(0xffffffffu, o, min(i0 + i, n - 1));
+        x[i] = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(oi) + 4 * lane);
+      }
+    };
+    const float l = p < parts ? *lse : -INFINITY;
+    load(0);
     const float m_new = fmaxf(m, warp_max(l));
     if (m_new == -INFINITY) continue;
     const float w = ex2((l - m_new) * 1.4426950408889634f), old = ex2((m - m_new) * 1.4426950408889634f);
     m = m_new;
     sum = sum * old + warp_sum(w);
     acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
-    // four rows in flight; a piece of weight 0 may have left none (whatever is
-    // there is read and not used)
     for (int i0 = 0; i0 < n; i0 += 4) {
-      float4 x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const unsigned long long oi = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), min(i0 + i, n - 1));
-        x[i] = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(oi) + 4 * lane);
-      }
+      if (i0 > 0) load(i0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float wi = i0 + i < n ? __shfl_sync(0xffffffffu, w, i0 + i) : 0.f;
