@@ -288,6 +288,12 @@ __device__ int2 unit_pieces(const PrefixAttnArgs& a, const int* start, const int
                    (at + tiles - 1) / share - at / share + 1);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -578,27 +584,30 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) x[i] = (i >= clo && i < chi) ? x[i] : -INFINITY;
           }
-          float mx[4] = {x[0], x[1], x[2], x[3]};
+          float mx[4] = {fmaxf(x[0], x[1]), fmaxf(x[2], x[3]), fmaxf(x[4], x[5]), fmaxf(x[6], x[7])};
 #pragma unroll
-          for (int i = 4; i < kKeys; i += 4)
+          for (int i = 8; i < kKeys; i += 8)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[i + k]);
-          const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], x[i + 2 * k], x[i + 2 * k + 1]);
+          const float tmax = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
           // the running max moves only when it grows by more than 2^8
           const bool rescale = live && (tmax - m_run) * c > kRescaleThreshold;
           const float m_new = rescale ? tmax : m_run;
           const float mc = m_new == -INFINITY ? 0.f : m_new * c;
-          uint32_t pk[32];
           float2 sm[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 e = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), c2, mc2);
-            const float2 q = make_float2(ex2(e.x), ex2(e.y));
-            sm[i & 1] = __fadd2_rn(sm[i & 1], q);
-            pk[i] = pack_bf16(q.x, q.y);
+          for (int hf = 0; hf < 2; ++hf) {  // the first half is stored under the second's exponentials
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = __ffma2_rn(make_float2(x[32 * hf + 2 * i], x[32 * hf + 2 * i + 1]), c2, mc2);
+              const float2 q = make_float2(ex2(e.x), ex2(e.y));
+              sm[i & 1] = __fadd2_rn(sm[i & 1], q);
+              pk[i] = pack_bf16(q.x, q.y);
+            }
+            ptx::tmem_st16(tS + (uint32_t)(16 * hf), pk);
           }
-          ptx::tmem_st32(tS, pk);
           const float alpha = rescale ? ex2(m_run * c - mc) : 1.f;  // 0 when m_run == -inf
           if (rescale) {
             l_run *= alpha;
