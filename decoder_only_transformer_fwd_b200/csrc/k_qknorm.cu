@@ -282,11 +282,18 @@ __global__ void __launch_bounds__(kThreads, MINB) k_qk_norm_rope_bwd(const __gri
 }
 
 // base^(-2i/D) / (2 pi) as fractions of 2^64, by repeated multiplication in
-// long double (64 factors: relative error below 2^-57)
+// long double (64 factors: relative error below 2^-57).  A thread keeps those of
+// the last base (a model has one); working them out takes 1 us of the host's time.
 void rope_freq(float base, RopeFreq* f) {
-  const long double ratio = expl(-logl((long double)base) / kHalf);
-  long double t = 0.15915494309189533576888376337251436203L;  // 1 / (2 pi)
-  for (int i = 0; i < kHalf; ++i, t *= ratio) f->turns[i] = (unsigned long long)(t * 18446744073709551616.0L);
+  static thread_local float last = 0.f;
+  static thread_local RopeFreq kept;
+  if (base != last) {
+    const long double ratio = expl(-logl((long double)base) / kHalf);
+    long double t = 0.15915494309189533576888376337251436203L;  // 1 / (2 pi)
+    for (int i = 0; i < kHalf; ++i, t *= ratio) kept.turns[i] = (unsigned long long)(t * 18446744073709551616.0L);
+    last = base;
+  }
+  *f = kept;
 }
 
 // Tokens per CTA: as many as leave a CTA for each SM and a third more, and a

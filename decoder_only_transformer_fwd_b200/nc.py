@@ -373,21 +373,33 @@ def _act_dtype(what: str, t):
     return NC_BF16 if t.dtype == torch.bfloat16 else NC_FP32
 
 
-def _take(what: str, name: str, t, shape, dtype, dev: int, packed: int = 0):
-    """Address of t, whose dimensions from `packed` (0 or the last two) on have
-    no gaps.  Runs on every call, next to kernels of a few microseconds: what a
-    correct call needs is compared here, the rest is left to _mismatch and
-    _packed."""
+# The checks below run on every call, next to kernels of a few microseconds:
+# what a correct call needs is compared here, in as few steps as it takes, and
+# the rest is left to _mismatch and _packed.
+
+def _take(what: str, name: str, t, shape, dtype, dev: int):
+    """Address of t, which is laid out without gaps."""
     if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _mismatch(what, name, t, shape, dtype)
-    if packed == 0:
-        if not t.is_contiguous():
-            _packed(what, name, t)
-    else:
-        st = t.stride()
-        if st[-1] != 1 or (packed == len(shape) - 2 and st[-2] != shape[-1]):
-            _packed(what, name, t, packed)
+    if not t.is_contiguous():
+        _packed(what, name, t)
     return t.data_ptr()
+
+
+def _take_rows(what: str, name: str, t, shape, dtype, dev: int, packed: int):
+    """(address, strides) of t, whose last one or two dimensions, from `packed` on, have no gaps."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _mismatch(what, name, t, shape, dtype)
+    st = t.stride()
+    if st[-1] != 1 or (packed == len(shape) - 2 and st[-2] != shape[-1]):
+        _packed(what, name, t, packed)
+    return t.data_ptr(), st
+
+
+def _current(t):
+    """The current CUDA device, for operands of which t is the first (None if that is not on one)."""
+    import torch
+    return torch._C._cuda_getDevice() if t.is_cuda else None
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -401,7 +413,7 @@ def _scratch(workspace, nbytes: int, like):
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        workspace = like.new_empty(nbytes, dtype=torch.uint8)
         return workspace, workspace.data_ptr(), nbytes
     if workspace.device != like.device or not workspace.is_contiguous():
         raise NcError("workspace: a contiguous tensor on the operands' device is needed")
@@ -416,8 +428,8 @@ def _heads_of(what: str, name: str, t):
 
 def _rows_of(what: str, name: str, t, shape, dtype, dev: int):
     """(address, row stride) of t [rows, heads, D]; a single row has any stride."""
-    p = _take(what, name, t, shape, dtype, dev, 1)
-    return p, t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+    p, st = _take_rows(what, name, t, shape, dtype, dev, 1)
+    return p, st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def nc_qk_norm_rope(q, k, positions, q_out, k_out, v=None, v_out=None, slots=None, alpha: float = 1.15,
@@ -426,7 +438,7 @@ def nc_qk_norm_rope(q, k, positions, q_out, k_out, v=None, v_out=None, slots=Non
     go to rows slots [N] (int32, -1 = not kept) of k_out and v_out [rows, H_kv, D], or to rows 0..N-1."""
     import torch
     what = "nc_qk_norm_rope"
-    dt, ty, dev = _act_dtype(what, q), q.dtype, torch.cuda.current_device() if q.is_cuda else None
+    dt, ty, dev = _act_dtype(what, q), q.dtype, _current(q)
     N, H, D = _heads_of(what, "q", q)
     Hkv, rows = _heads_of(what, "k", k)[1], _heads_of(what, "k_out", k_out)[0]
     if (v is None) != (v_out is None):
@@ -455,7 +467,7 @@ def nc_qk_norm_rope_backward(q, k, positions, dq_hat, dk_hat, out_dq, out_dk, al
     """Gradients of q [N, H, D] and k [N, H_kv, D] from those of nc_qk_norm_rope's qhat and khat."""
     import torch
     what = "nc_qk_norm_rope_backward"
-    dt, ty, dev = _act_dtype(what, q), q.dtype, torch.cuda.current_device() if q.is_cuda else None
+    dt, ty, dev = _act_dtype(what, q), q.dtype, _current(q)
     N, H, D = _heads_of(what, "q", q)
     Hkv = _heads_of(what, "k", k)[1]
     pq, ldq = _rows_of(what, "q", q, (N, H, D), ty, dev)
@@ -482,9 +494,13 @@ def _prefix_attention_bytes(*sizes) -> int:
     return nc_prefix_attention_workspace_bytes(*sizes)
 
 
+_SIDES = {side: (f"k_{side}", f"v_{side}", f"{side}_lens") for side in ("prefix", "suffix")}
+
+
 def _cache_of(what: str, side: str, k, v, lens, n, D: int, dev: int):
     """One side's caches [sequences, keys, H_kv, D]: (k, v, strides, lens, sequences, keys, H_kv)."""
     import torch
+    names = _SIDES[side]
     if k is None:
         if v is not None or lens is not None:
             raise NcError(f"{what}: k, v and lengths of the {side} come together")
@@ -496,10 +512,9 @@ def _cache_of(what: str, side: str, k, v, lens, n, D: int, dev: int):
     seqs, cap, Hkv, Dk = shape = tuple(k.shape)
     if Dk != D or (n is not None and seqs != n):
         raise NcError(f"{what}: k_{side} has shape {shape}, expected ({n or 'G'}, keys, H_kv, {D})")
-    pk = _take(what, f"k_{side}", k, shape, torch.bfloat16, dev, 2)
-    pv = _take(what, f"v_{side}", v, shape, torch.bfloat16, dev, 2)
-    pl = _take(what, f"{side}_lens", lens, (seqs,), torch.int32, dev)
-    sk, sv = k.stride(), v.stride()
+    pk, sk = _take_rows(what, names[0], k, shape, torch.bfloat16, dev, 2)
+    pv, sv = _take_rows(what, names[1], v, shape, torch.bfloat16, dev, 2)
+    pl = _take(what, names[2], lens, (seqs,), torch.int32, dev)
     if (cap > 1 and sk[1] != sv[1]) or (seqs > 1 and sk[0] != sv[0]):
         raise NcError(f"{what}: k_{side} and v_{side} must have the same strides")
     if cap == 0:
@@ -508,9 +523,8 @@ def _cache_of(what: str, side: str, k, v, lens, n, D: int, dev: int):
     return pk, pv, ld, sk[0] if seqs > 1 else ld * cap, pl, seqs, cap, Hkv
 
 
-def _even_rows(what: str, name: str, t, outer: int, inner: int, width: int) -> int:
-    """Stride between consecutive rows of t [outer, inner, ...], which must be evenly spaced."""
-    st = t.stride()
+def _even_rows(what: str, name: str, st, outer: int, inner: int, width: int) -> int:
+    """Stride between consecutive rows of a tensor [outer, inner, ...] of strides st, which must be evenly spaced."""
     ld = st[1] if inner > 1 else (st[0] if outer > 1 else width)
     if outer > 1 and inner > 1 and st[0] != inner * ld:
         raise NcError(f"{what}: {name}'s rows must be evenly spaced (strides {st})")
@@ -524,11 +538,11 @@ def nc_prefix_attention(q, k_prefix, v_prefix, prefix_lens, k_suffix, v_suffix, 
     (suffix_lens [B] int32); one side may be None.  out [B, Tq, H, D], out_lse [B, Tq, H] fp32."""
     import torch
     what = "nc_prefix_attention"
-    dev = torch.cuda.current_device() if q.is_cuda else None
+    dev = _current(q)
     if q.dim() != 4:
         raise NcError(f"{what}: q is [B, Tq, H, D]")
     B, Tq, H, D = shape = tuple(q.shape)
-    pq = _take(what, "q", q, shape, torch.bfloat16, dev, 2)
+    pq, sq = _take_rows(what, "q", q, shape, torch.bfloat16, dev, 2)
     kp, vp, ldp, lsp, pl, G, P, hp = _cache_of(what, "prefix", k_prefix, v_prefix, prefix_lens, None, D, dev)
     ks, vs, lds, lss, sl, _, S, hs = _cache_of(what, "suffix", k_suffix, v_suffix, suffix_lens, B, D, dev)
     Hkv = hp if hs is None else hs
@@ -536,7 +550,7 @@ def nc_prefix_attention(q, k_prefix, v_prefix, prefix_lens, k_suffix, v_suffix, 
         raise NcError(f"{what}: " + ("there are no keys" if Hkv is None else "prefix and suffix differ in key heads"))
     po = _take(what, "out", out, shape, torch.bfloat16, dev)
     pe = None if out_lse is None else _take(what, "out_lse", out_lse, (B, Tq, H), torch.float32, dev)
-    ldq = _even_rows(what, "q", q, B, Tq, H * D)
+    ldq = _even_rows(what, "q", sq, B, Tq, H * D)
     scale = D ** -0.5 if softmax_scale is None else softmax_scale
     workspace, pw, nbytes = _scratch(workspace, _prefix_attention_bytes(B, G, Tq, H, Hkv, P, S, window), q)
     rc = lib().nc_prefix_attention(pq, ldq, kp, vp, ldp, lsp, pl, ks, vs, lds, lss, sl, po, pe, B, G, Tq, H, Hkv, D,
@@ -553,22 +567,22 @@ def nc_policy_loss(logits, targets, advantages, out_stats, out_logp, out_dlogits
     import torch
     what = "nc_policy_loss"
     dt, ty, f32 = _act_dtype(what, logits), logits.dtype, torch.float32
-    dev = torch.cuda.current_device() if logits.is_cuda else None
+    dev = _current(logits)
     if logits.dim() != 3:
         raise NcError(f"{what}: logits are [B, T, V]")
     B, T, V = shape = tuple(logits.shape)
     bt, per_token = (B, T), advantages.dim() == 2
-    pz = _take(what, "logits", logits, shape, ty, dev, 2)
+    pz, sz = _take_rows(what, "logits", logits, shape, ty, dev, 2)
     py = _take(what, "targets", targets, bt, torch.int32, dev)
     pa = _take(what, "advantages", advantages, bt if per_token else (B,), f32, dev)
     ps = _take(what, "out_stats", out_stats, (3,), f32, dev)
     pl = _take(what, "out_logp", out_logp, bt, f32, dev)
     po = None if old_logp is None else _take(what, "old_logp", old_logp, bt, f32, dev)
     pr = None if ref_logp is None else _take(what, "ref_logp", ref_logp, bt, f32, dev)
-    ldl, pd, lddl = _even_rows(what, "logits", logits, B, T, V), None, 0
+    ldl, pd, lddl = _even_rows(what, "logits", sz, B, T, V), None, 0
     if out_dlogits is not None:
-        pd = _take(what, "out_dlogits", out_dlogits, shape, ty, dev, 2)
-        lddl = _even_rows(what, "out_dlogits", out_dlogits, B, T, V)
+        pd, sd = _take_rows(what, "out_dlogits", out_dlogits, shape, ty, dev, 2)
+        lddl = _even_rows(what, "out_dlogits", sd, B, T, V)
     workspace, pw, nbytes = _scratch(workspace, _policy_bytes(), logits)
     rc = lib().nc_policy_loss(pz, ldl, py, pa, per_token, po, pr, B, T, V, clip_low, clip_high, kl_beta, norm, ps, pl, pd, lddl,
                               dt, pw, nbytes, _raw_stream(stream, dev))
