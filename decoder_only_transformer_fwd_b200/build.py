@@ -1,4 +1,5 @@
-"""Build libnc.so in-tree for sm_100a with nvcc (one object per .cu, then link).
+"""Build libnc.so in-tree for sm_100a with nvcc (one object per .cu, then link),
+and _ncpy.so, the native part of the Python binding (csrc/nc_py.cpp), with g++.
 
     python -m decoder_only_transformer_fwd_b200.build [--force] [--verbose]
 
@@ -11,15 +12,18 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnc.so")
+PYLIB = os.path.join(PKG, "_ncpy.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -40,6 +44,27 @@ def _stale(src, obj, hdr_mtime):
         return True
     t = os.path.getmtime(obj)
     return os.path.getmtime(src) > t or hdr_mtime > t
+
+
+def build_py(force: bool = False, verbose: bool = False) -> str:
+    """_ncpy.so against torch's headers and libraries (which are loaded by the time it is) and libnc.so beside it."""
+    src = os.path.join(CSRC, "nc_py.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(ROOT, "include", "nc.h")))
+    if not force and os.path.exists(PYLIB) and os.path.getmtime(PYLIB) > newest:
+        return PYLIB
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{d}" for d in include), src, "-o", PYLIB,
+           f"-L{torch_dir}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-L{PKG}", "-l:libnc.so",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed:\n{r.stderr}")
+    if verbose:
+        sys.stderr.write(f"[g++] nc_py.cpp\n{r.stderr}")
+    return PYLIB
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -70,6 +95,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
+    build_py(force=force, verbose=verbose)
     return LIB
 
 

@@ -2,8 +2,9 @@
 // rows, and its gradient.
 //
 // "The Mathematics of Karpathy's nanochat", §QK-Norm with Sharpening, §Rotary
-// Position Embeddings: with R(t) the half-split rotation by t theta_i,
-// theta_i = base^(-2i/D),
+// Position Embeddings: with R(t) the half-split rotation (u1 cos + u2 sin,
+// -u1 sin + u2 cos) by t theta_i, theta_i = base^(-2i/D) (`reverse`: by the
+// negated angles, as many other half-split models turn),
 //   y = alpha R x / rho,   rho = sqrt(mean(x^2) + eps)
 // (the rotation keeps the norm, so rho is taken from x).  Its gradient, with
 // b = R^T dy,
@@ -108,8 +109,8 @@ __device__ __forceinline__ float sum8(float v, unsigned mask) {
 // cos and sin of a position's 64 angles into shared memory, one angle per
 // thread: the upper 32 bits of position * turns are the phase in turns to
 // 2^-32, a signed fraction in [-1/2, 1/2)
-__device__ __forceinline__ void fill_angles(const RopeFreq& f, const int32_t* positions, int n0, int ntok, float* cs,
-                                            int* status) {
+__device__ __forceinline__ void fill_angles(const RopeFreq& f, const int32_t* positions, int reverse, int n0, int ntok,
+                                            float* cs, int* status) {
   for (int i = threadIdx.x; i < ntok * kHalf; i += kThreads) {
     int pos = positions[n0 + i / kHalf];
     if (pos < 0) {
@@ -119,7 +120,7 @@ __device__ __forceinline__ void fill_angles(const RopeFreq& f, const int32_t* po
     const unsigned long long ph = (unsigned long long)(unsigned)pos * f.turns[i % kHalf];
     const float turn = (float)(int)(unsigned)(ph >> 32) * 2.3283064365386963e-10f;  // 2^-32
     float s, c;
-    sincospif(2.0f * turn, &s, &c);
+    sincospif(reverse ? -2.0f * turn : 2.0f * turn, &s, &c);
     cs[(i / kHalf) * 2 * kHalf + i % kHalf] = c;
     cs[(i / kHalf) * 2 * kHalf + kHalf + i % kHalf] = s;
   }
@@ -143,7 +144,7 @@ struct FwdArgs {
   T *qo, *ko, *vo;
   long long ldq, ldk, ldv, ldqo, ldko, ldvo;  // row strides, elements
   const int32_t *positions, *slots;
-  int N, H, Hkv, tok;  // tok: tokens per CTA
+  int N, H, Hkv, reverse, tok;  // tok: tokens per CTA
   long long out_rows;
   float alpha, eps;
   int* status;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant
   Raw<T> next;
   if (live && h < a.H + kept) next.load(source(h), j);
   long long slot = live ? (a.slots != nullptr ? (long long)a.slots[n] : (long long)n) : 0;
-  fill_angles(a.f, a.positions, n0, ntok, cs, a.status);
+  fill_angles(a.f, a.positions, a.reverse, n0, ntok, cs, a.status);
   __syncthreads();
   if (!live) return;
   const unsigned mask = 0xffu << ((threadIdx.x & 31) & ~7);
@@ -203,8 +204,8 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float u = x.a[i], w = x.b[i];
-        x.a[i] = r * (u * c[i] - w * s[i]);
-        x.b[i] = r * (w * c[i] + u * s[i]);
+        x.a[i] = r * (u * c[i] + w * s[i]);
+        x.b[i] = r * (w * c[i] - u * s[i]);
       }
       raw.set(x);
     }
@@ -218,7 +219,7 @@ struct BwdArgs {
   T *dq, *dk;
   long long ldq, ldk, ldgq, ldgk, lddq, lddk;
   const int32_t* positions;
-  int N, H, Hkv, tok;
+  int N, H, Hkv, reverse, tok;
   float alpha, eps;
   int* status;
   RopeFreq f;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_qk_norm_rope_bwd(const __gri
     ng.load(hk < 0 ? a.gq + n * a.ldgq + h * kD : a.gk + n * a.ldgk + hk * kD, j);
   };
   if (live && h < heads) load(h);
-  fill_angles(a.f, a.positions, n0, ntok, cs, a.status);
+  fill_angles(a.f, a.positions, a.reverse, n0, ntok, cs, a.status);
   __syncthreads();
   if (!live) return;
   const unsigned mask = 0xffu << ((threadIdx.x & 31) & ~7);
@@ -261,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, MINB) k_qk_norm_rope_bwd(const __gri
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float u = g.a[i], w = g.b[i];
-      g.a[i] = u * c[i] + w * s[i];
-      g.b[i] = w * c[i] - u * s[i];
+      g.a[i] = u * c[i] - w * s[i];
+      g.b[i] = w * c[i] + u * s[i];
       ss += x.a[i] * x.a[i] + x.b[i] * x.b[i];
       dot += x.a[i] * g.a[i] + x.b[i] * g.b[i];
     }
@@ -315,7 +316,7 @@ static void run_fwd(const QkNormArgs& p, int num_sms, cudaStream_t st) {
   a.qo = static_cast<T*>(p.q_out), a.ko = static_cast<T*>(p.k_out), a.vo = static_cast<T*>(p.v_out);
   a.ldq = p.ldq, a.ldk = p.ldk, a.ldv = p.ldv, a.ldqo = p.ldqo, a.ldko = p.ldko, a.ldvo = p.ldvo;
   a.positions = p.positions, a.slots = p.slots;
-  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.tok = tokens_per_cta(p.N, p.H + (p.v != nullptr ? 2 : 1) * p.Hkv, num_sms);
+  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.reverse = p.reverse, a.tok = tokens_per_cta(p.N, p.H + (p.v != nullptr ? 2 : 1) * p.Hkv, num_sms);
   a.out_rows = p.out_rows, a.alpha = p.alpha, a.eps = p.eps, a.status = p.status;
   rope_freq(p.rope_base, &a.f);
   LaunchScope scope_(KK_QK_NORM_ROPE, st);
@@ -337,7 +338,7 @@ static void run_bwd(const QkNormArgs& p, int num_sms, cudaStream_t st) {
   a.dq = static_cast<T*>(p.q_out), a.dk = static_cast<T*>(p.k_out);
   a.ldq = p.ldq, a.ldk = p.ldk, a.ldgq = p.ldgq, a.ldgk = p.ldgk, a.lddq = p.ldqo, a.lddk = p.ldko;
   a.positions = p.positions;
-  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.tok = tokens_per_cta(p.N, p.H + p.Hkv, num_sms);
+  a.N = p.N, a.H = p.H, a.Hkv = p.Hkv, a.reverse = p.reverse, a.tok = tokens_per_cta(p.N, p.H + p.Hkv, num_sms);
   a.alpha = p.alpha, a.eps = p.eps, a.status = p.status;
   rope_freq(p.rope_base, &a.f);
   LaunchScope scope_(KK_QK_NORM_ROPE, st);

@@ -862,7 +862,7 @@ static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 // Checks that the two directions of QK-norm share; NC_OK or the error.
 static int qk_norm_check(const QkNormArgs& p, int D, int dtype) {
   if (!(p.alpha > 0.f) || !std::isfinite(p.alpha) || !(p.rope_base >= 1.f) || !std::isfinite(p.rope_base) ||
-      !(p.eps >= 0.f) || !std::isfinite(p.eps))
+      !(p.eps >= 0.f) || !std::isfinite(p.eps) || (p.reverse != 0 && p.reverse != 1))
     return NC_ERR_ARG;
   if (dtype != NC_BF16 && dtype != NC_FP32) return NC_ERR_ARG;
   if (p.N < 0 || p.H <= 0 || p.Hkv <= 0 || D != 128 || p.H % p.Hkv != 0 || p.H > (1 << 20)) return NC_ERR_SHAPE;
@@ -872,14 +872,14 @@ static int qk_norm_check(const QkNormArgs& p, int D, int dtype) {
 int nc_qk_norm_rope(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
                     const int32_t* positions, const int32_t* slots, int N, int H, int Hkv, int D, void* q_out,
                     long long ldqo, void* k_out, long long ldko, void* v_out, long long ldvo, long long out_rows,
-                    float alpha, float rope_base, float eps, int dtype, void* stream) {
+                    float alpha, float rope_base, int reverse, float eps, int dtype, void* stream) {
   t_launches = 0;
   QkNormArgs p;
   memset(&p, 0, sizeof(p));
   p.q = q, p.k = k, p.v = v, p.q_out = q_out, p.k_out = k_out, p.v_out = v_out;
   p.ldq = ldq, p.ldk = ldk, p.ldv = ldv, p.ldqo = ldqo, p.ldko = ldko, p.ldvo = ldvo;
   p.positions = positions, p.slots = slots, p.N = N, p.H = H, p.Hkv = Hkv, p.out_rows = out_rows;
-  p.alpha = alpha, p.rope_base = rope_base, p.eps = eps;
+  p.alpha = alpha, p.rope_base = rope_base, p.reverse = reverse, p.eps = eps;
   if (!q || !k || !positions || !q_out || !k_out || (v == nullptr) != (v_out == nullptr)) return NC_ERR_ARG;
   const int rc = qk_norm_check(p, D, dtype);
   if (rc != NC_OK) return rc;
@@ -903,14 +903,14 @@ int nc_qk_norm_rope(const void* q, long long ldq, const void* k, long long ldk, 
 int nc_qk_norm_rope_backward(const void* q, long long ldq, const void* k, long long ldk, const int32_t* positions,
                              const void* dq_hat, long long ldgq, const void* dk_hat, long long ldgk, int N, int H,
                              int Hkv, int D, void* out_dq, long long lddq, void* out_dk, long long lddk, float alpha,
-                             float rope_base, float eps, int dtype, void* stream) {
+                             float rope_base, int reverse, float eps, int dtype, void* stream) {
   t_launches = 0;
   QkNormArgs p;
   memset(&p, 0, sizeof(p));
   p.q = q, p.k = k, p.dq_hat = dq_hat, p.dk_hat = dk_hat, p.q_out = out_dq, p.k_out = out_dk;
   p.ldq = ldq, p.ldk = ldk, p.ldgq = ldgq, p.ldgk = ldgk, p.ldqo = lddq, p.ldko = lddk;
   p.positions = positions, p.N = N, p.H = H, p.Hkv = Hkv;
-  p.alpha = alpha, p.rope_base = rope_base, p.eps = eps;
+  p.alpha = alpha, p.rope_base = rope_base, p.reverse = reverse, p.eps = eps;
   if (!q || !k || !positions || !dq_hat || !dk_hat || !out_dq || !out_dk) return NC_ERR_ARG;
   const int rc = qk_norm_check(p, D, dtype);
   if (rc != NC_OK) return rc;

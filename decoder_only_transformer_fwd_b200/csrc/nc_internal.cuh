@@ -217,7 +217,7 @@ struct QkNormArgs {
   void *q_out, *k_out, *v_out;
   long long ldq, ldk, ldv, ldgq, ldgk, ldqo, ldko, ldvo;
   const int32_t *positions, *slots;
-  int N, H, Hkv;
+  int N, H, Hkv, reverse;
   long long out_rows;
   float alpha, rope_base, eps;
   int* status;

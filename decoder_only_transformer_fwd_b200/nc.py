@@ -1,4 +1,6 @@
-"""ctypes binding of libnc.so (include/nc.h).
+"""ctypes binding of libnc.so (include/nc.h); the calls of the sampling operators,
+whose kernels take a few microseconds, check and pass their tensors in native
+code (csrc/nc_py.cpp).
 
 Argument marshalling only: device buffers are torch tensors (PyTorch is used
 for allocation and streams), every step of the forward pass runs in the
@@ -8,7 +10,6 @@ build raises immediately; there is no fallback path.
 from __future__ import annotations
 
 import ctypes as C
-import functools
 import os
 
 import numpy as np
@@ -52,6 +53,7 @@ class NcError(RuntimeError):
 
 
 _lib = None
+_ncpy = None
 
 _SIGS = {
     "nc_init_config": (C.c_int, [C.POINTER(nc_config), C.c_int, C.c_int, C.c_int, C.c_char_p, C.c_int, C.c_int]),
@@ -97,10 +99,11 @@ _SIGS = {
     "nc_head_backward": (C.c_int, [C.POINTER(nc_params), C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
                                    C.c_void_p, C.c_size_t, C.c_void_p]),
     "nc_qk_norm_rope": (C.c_int, [C.c_void_p, C.c_longlong] * 3 + [C.c_void_p] * 2 + [C.c_int] * 4
-                        + [C.c_void_p, C.c_longlong] * 3 + [C.c_longlong] + [C.c_float] * 3 + [C.c_int, C.c_void_p]),
+                        + [C.c_void_p, C.c_longlong] * 3 + [C.c_longlong] + [C.c_float] * 2 + [C.c_int, C.c_float]
+                        + [C.c_int, C.c_void_p]),
     "nc_qk_norm_rope_backward": (C.c_int, [C.c_void_p, C.c_longlong] * 2 + [C.c_void_p] + [C.c_void_p, C.c_longlong] * 2
-                                 + [C.c_int] * 4 + [C.c_void_p, C.c_longlong] * 2 + [C.c_float] * 3
-                                 + [C.c_int, C.c_void_p]),
+                                 + [C.c_int] * 4 + [C.c_void_p, C.c_longlong] * 2 + [C.c_float] * 2
+                                 + [C.c_int, C.c_float, C.c_int, C.c_void_p]),
     "nc_prefix_attention_workspace_bytes": (C.c_size_t, [C.c_int] * 8),
     "nc_prefix_attention": (C.c_int, [C.c_void_p, C.c_longlong]
                             + ([C.c_void_p] * 2 + [C.c_longlong] * 2 + [C.c_void_p]) * 2 + [C.c_void_p] * 2
@@ -341,194 +344,42 @@ def nc_prefix_ce(x, w_u, targets, out_loss, vocab: int, widths, eps: float = 1e-
                               cap, _ptr(workspace), nbytes, _stream(stream)), "nc_prefix_ce")
 
 
-def _mismatch(what: str, name: str, t, shape, dtype):
-    """Raises for a tensor that is not what the call takes.  All tensors must
-    be on the current CUDA device: the call runs there, on one of its streams."""
-    import torch
-    if t is None:
-        raise NcError(f"{what}: {name} is missing")
-    if t.dtype != dtype:
-        raise NcError(f"{what}: {name} is {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise NcError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda:
-        raise NcError(f"{what}: {name} is not on a CUDA device")
-    raise NcError(f"{what}: {name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _packed(what: str, name: str, t, first: int = 0):
-    """t's dimensions from `first` on are laid out without gaps."""
-    want = 1
-    for n, s in zip(reversed(t.shape[first:]), reversed(t.stride()[first:])):
-        if n > 1 and s != want:
-            raise NcError(f"{what}: {name} has strides {tuple(t.stride())}: "
-                          f"its last {t.dim() - first} dimension(s) must be contiguous")
-        want *= n
-
-
-def _act_dtype(what: str, t):
-    import torch
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise NcError(f"{what}: {t.dtype} is not supported (bfloat16 or float32)")
-    return NC_BF16 if t.dtype == torch.bfloat16 else NC_FP32
-
-
-# The checks below run on every call, next to kernels of a few microseconds:
-# what a correct call needs is compared here, in as few steps as it takes, and
-# the rest is left to _mismatch and _packed.
-
-def _take(what: str, name: str, t, shape, dtype, dev: int):
-    """Address of t, which is laid out without gaps."""
-    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _mismatch(what, name, t, shape, dtype)
-    if not t.is_contiguous():
-        _packed(what, name, t)
-    return t.data_ptr()
-
-
-def _take_rows(what: str, name: str, t, shape, dtype, dev: int, packed: int):
-    """(address, strides) of t, whose last one or two dimensions, from `packed` on, have no gaps."""
-    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _mismatch(what, name, t, shape, dtype)
-    st = t.stride()
-    if st[-1] != 1 or (packed == len(shape) - 2 and st[-2] != shape[-1]):
-        _packed(what, name, t, packed)
-    return t.data_ptr(), st
-
-
-def _current(t):
-    """The current CUDA device, for operands of which t is the first (None if that is not on one)."""
-    import torch
-    return torch._C._cuda_getDevice() if t.is_cuda else None
-
-
-def _raw_stream(stream, dev: int) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _scratch(workspace, nbytes: int, like):
-    """(workspace, its address, its bytes): the caller's, or a new one of nbytes."""
-    import torch
-    if workspace is None:
-        if nbytes == 0:
-            return None, None, 0
-        workspace = like.new_empty(nbytes, dtype=torch.uint8)
-        return workspace, workspace.data_ptr(), nbytes
-    if workspace.device != like.device or not workspace.is_contiguous():
-        raise NcError("workspace: a contiguous tensor on the operands' device is needed")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _heads_of(what: str, name: str, t):
-    if t.dim() != 3:
-        raise NcError(f"{what}: {name} is [N, heads, D]")
-    return t.shape
-
-
-def _rows_of(what: str, name: str, t, shape, dtype, dev: int):
-    """(address, row stride) of t [rows, heads, D]; a single row has any stride."""
-    p, st = _take_rows(what, name, t, shape, dtype, dev, 1)
-    return p, st[0] if shape[0] > 1 else shape[1] * shape[2]
+def _native():
+    """The native part of the binding (csrc/nc_py.cpp), loaded once: it checks the tensors of the calls below, whose
+    kernels take a few microseconds, and passes them on.  There is no fallback path."""
+    global _ncpy
+    if _ncpy is None:
+        import torch  # noqa: F401  (its libraries come first)
+        lib()
+        try:
+            from . import _ncpy as m
+        except ImportError as e:
+            raise NcError("_ncpy.so is missing or does not load: build it with "
+                          f"`python -m decoder_only_transformer_fwd_b200.build` ({e})") from e
+        m.set_error(NcError)
+        _ncpy = m
+    return _ncpy
 
 
 def nc_qk_norm_rope(q, k, positions, q_out, k_out, v=None, v_out=None, slots=None, alpha: float = 1.15,
-                    rope_base: float = 100000.0, eps: float = 1e-6, stream=None):
+                    rope_base: float = 100000.0, eps: float = 1e-6, reverse: bool = False, stream=None):
     """qhat [N, H, D] and khat of tokens q [N, H, D], k [N, H_kv, D] at positions [N] (int32); khat and v
-    go to rows slots [N] (int32, -1 = not kept) of k_out and v_out [rows, H_kv, D], or to rows 0..N-1."""
-    import torch
-    what = "nc_qk_norm_rope"
-    dt, ty, dev = _act_dtype(what, q), q.dtype, _current(q)
-    N, H, D = _heads_of(what, "q", q)
-    Hkv, rows = _heads_of(what, "k", k)[1], _heads_of(what, "k_out", k_out)[0]
-    if (v is None) != (v_out is None):
-        raise NcError(f"{what}: v and v_out come together")
-    pq, ldq = _rows_of(what, "q", q, (N, H, D), ty, dev)
-    pk, ldk = _rows_of(what, "k", k, (N, Hkv, D), ty, dev)
-    po, ldo = _rows_of(what, "q_out", q_out, (N, H, D), ty, dev)
-    pc, ldc = _rows_of(what, "k_out", k_out, (rows, Hkv, D), ty, dev)
-    pv = pd = None
-    ldv = ldd = 0
-    if v is not None:
-        pv, ldv = _rows_of(what, "v", v, (N, Hkv, D), ty, dev)
-        pd, ldd = _rows_of(what, "v_out", v_out, (rows, Hkv, D), ty, dev)
-    pp = _take(what, "positions", positions, (N,), torch.int32, dev)
-    ps = None if slots is None else _take(what, "slots", slots, (N,), torch.int32, dev)
-    if N == 0:
-        return
-    rc = lib().nc_qk_norm_rope(pq, ldq, pk, ldk, pv, ldv, pp, ps, N, H, Hkv, D, po, ldo, pc, ldc, pd, ldd, rows,
-                               alpha, rope_base, eps, dt, _raw_stream(stream, dev))
-    if rc:
-        _check(rc, what)
+    go to rows slots [N] (int32, -1 = not kept) of k_out and v_out [rows, H_kv, D], or to rows 0..N-1.
+    RoPE turns as in nc_forward, or with negated angles (reverse).  Rows may be strided (slices of one projection's
+    output).  Tensors of this and the calls below must be on the current CUDA device; a tensor of another type, shape or layout is refused with an NcError."""
+    (_ncpy or _native()).qk_norm_rope(q, k, positions, q_out, k_out, v, v_out, slots, alpha, rope_base, reverse, eps,
+                                       stream)
 
 
 def nc_qk_norm_rope_backward(q, k, positions, dq_hat, dk_hat, out_dq, out_dk, alpha: float = 1.15,
-                             rope_base: float = 100000.0, eps: float = 1e-6, stream=None):
+                             rope_base: float = 100000.0, eps: float = 1e-6, reverse: bool = False, stream=None):
     """Gradients of q [N, H, D] and k [N, H_kv, D] from those of nc_qk_norm_rope's qhat and khat."""
-    import torch
-    what = "nc_qk_norm_rope_backward"
-    dt, ty, dev = _act_dtype(what, q), q.dtype, _current(q)
-    N, H, D = _heads_of(what, "q", q)
-    Hkv = _heads_of(what, "k", k)[1]
-    pq, ldq = _rows_of(what, "q", q, (N, H, D), ty, dev)
-    pk, ldk = _rows_of(what, "k", k, (N, Hkv, D), ty, dev)
-    pg, ldg = _rows_of(what, "dq_hat", dq_hat, (N, H, D), ty, dev)
-    ph, ldh = _rows_of(what, "dk_hat", dk_hat, (N, Hkv, D), ty, dev)
-    pd, ldd = _rows_of(what, "out_dq", out_dq, (N, H, D), ty, dev)
-    pe, lde = _rows_of(what, "out_dk", out_dk, (N, Hkv, D), ty, dev)
-    pp = _take(what, "positions", positions, (N,), torch.int32, dev)
-    if N == 0:
-        return
-    rc = lib().nc_qk_norm_rope_backward(pq, ldq, pk, ldk, pp, pg, ldg, ph, ldh, N, H, Hkv, D, pd, ldd, pe, lde, alpha,
-                                        rope_base, eps, dt, _raw_stream(stream, dev))
-    if rc:
-        _check(rc, what)
+    (_ncpy or _native()).qk_norm_rope_backward(q, k, positions, dq_hat, dk_hat, out_dq, out_dk, alpha, rope_base, reverse,
+                                                eps, stream)
 
 
 def nc_prefix_attention_workspace_bytes(B, G, Tq, H, Hkv, P_max, S_max, window: int = 0) -> int:
     return int(lib().nc_prefix_attention_workspace_bytes(B, G, Tq, H, Hkv, P_max, S_max, window))
-
-
-@functools.lru_cache(maxsize=256)
-def _prefix_attention_bytes(*sizes) -> int:
-    return nc_prefix_attention_workspace_bytes(*sizes)
-
-
-_SIDES = {side: (f"k_{side}", f"v_{side}", f"{side}_lens") for side in ("prefix", "suffix")}
-
-
-def _cache_of(what: str, side: str, k, v, lens, n, D: int, dev: int):
-    """One side's caches [sequences, keys, H_kv, D]: (k, v, strides, lens, sequences, keys, H_kv)."""
-    import torch
-    names = _SIDES[side]
-    if k is None:
-        if v is not None or lens is not None:
-            raise NcError(f"{what}: k, v and lengths of the {side} come together")
-        return None, None, 0, 0, None, 1, 0, None
-    if v is None or lens is None:
-        raise NcError(f"{what}: k, v and lengths of the {side} come together")
-    if k.dim() != 4:
-        raise NcError(f"{what}: k_{side} is [sequences, keys, H_kv, D]")
-    seqs, cap, Hkv, Dk = shape = tuple(k.shape)
-    if Dk != D or (n is not None and seqs != n):
-        raise NcError(f"{what}: k_{side} has shape {shape}, expected ({n or 'G'}, keys, H_kv, {D})")
-    pk, sk = _take_rows(what, names[0], k, shape, torch.bfloat16, dev, 2)
-    pv, sv = _take_rows(what, names[1], v, shape, torch.bfloat16, dev, 2)
-    pl = _take(what, names[2], lens, (seqs,), torch.int32, dev)
-    if (cap > 1 and sk[1] != sv[1]) or (seqs > 1 and sk[0] != sv[0]):
-        raise NcError(f"{what}: k_{side} and v_{side} must have the same strides")
-    if cap == 0:
-        return None, None, 0, 0, None, seqs, 0, Hkv
-    ld = sk[1] if cap > 1 else Hkv * D
-    return pk, pv, ld, sk[0] if seqs > 1 else ld * cap, pl, seqs, cap, Hkv
-
-
-def _even_rows(what: str, name: str, st, outer: int, inner: int, width: int) -> int:
-    """Stride between consecutive rows of a tensor [outer, inner, ...] of strides st, which must be evenly spaced."""
-    ld = st[1] if inner > 1 else (st[0] if outer > 1 else width)
-    if outer > 1 and inner > 1 and st[0] != inner * ld:
-        raise NcError(f"{what}: {name}'s rows must be evenly spaced (strides {st})")
-    return ld
 
 
 def nc_prefix_attention(q, k_prefix, v_prefix, prefix_lens, k_suffix, v_suffix, suffix_lens, out, out_lse=None,
@@ -536,27 +387,12 @@ def nc_prefix_attention(q, k_prefix, v_prefix, prefix_lens, k_suffix, v_suffix, 
     """Attention of q [B, Tq, H, D] over the prefixes k_prefix, v_prefix [G, P_max, H_kv, D] that consecutive
     rows share (prefix_lens [G] int32) and the rows' own k_suffix, v_suffix [B, S_max, H_kv, D]
     (suffix_lens [B] int32); one side may be None.  out [B, Tq, H, D], out_lse [B, Tq, H] fp32."""
-    import torch
-    what = "nc_prefix_attention"
-    dev = _current(q)
-    if q.dim() != 4:
-        raise NcError(f"{what}: q is [B, Tq, H, D]")
-    B, Tq, H, D = shape = tuple(q.shape)
-    pq, sq = _take_rows(what, "q", q, shape, torch.bfloat16, dev, 2)
-    kp, vp, ldp, lsp, pl, G, P, hp = _cache_of(what, "prefix", k_prefix, v_prefix, prefix_lens, None, D, dev)
-    ks, vs, lds, lss, sl, _, S, hs = _cache_of(what, "suffix", k_suffix, v_suffix, suffix_lens, B, D, dev)
-    Hkv = hp if hs is None else hs
-    if Hkv is None or (hp is not None and hp != Hkv):
-        raise NcError(f"{what}: " + ("there are no keys" if Hkv is None else "prefix and suffix differ in key heads"))
-    po = _take(what, "out", out, shape, torch.bfloat16, dev)
-    pe = None if out_lse is None else _take(what, "out_lse", out_lse, (B, Tq, H), torch.float32, dev)
-    ldq = _even_rows(what, "q", sq, B, Tq, H * D)
-    scale = D ** -0.5 if softmax_scale is None else softmax_scale
-    workspace, pw, nbytes = _scratch(workspace, _prefix_attention_bytes(B, G, Tq, H, Hkv, P, S, window), q)
-    rc = lib().nc_prefix_attention(pq, ldq, kp, vp, ldp, lsp, pl, ks, vs, lds, lss, sl, po, pe, B, G, Tq, H, Hkv, D,
-                                   P, S, window, scale, pw, nbytes, _raw_stream(stream, dev))
-    if rc:
-        _check(rc, what)
+    (_ncpy or _native()).prefix_attention(q, k_prefix, v_prefix, prefix_lens, k_suffix, v_suffix, suffix_lens, out, out_lse,
+                                          window, softmax_scale, workspace, stream)
+
+
+def nc_policy_loss_workspace_bytes() -> int:
+    return int(lib().nc_policy_loss_workspace_bytes())
 
 
 def nc_policy_loss(logits, targets, advantages, out_stats, out_logp, out_dlogits=None, old_logp=None, ref_logp=None,
@@ -564,35 +400,8 @@ def nc_policy_loss(logits, targets, advantages, out_stats, out_logp, out_dlogits
                    stream=None):
     """Clipped policy loss of logits [B, T, V] (rows may be strided) at targets [B, T] (-1 = none) with advantages
     [B] or [B, T]: out_stats [3] (loss, mean KL, clipped share), out_logp [B, T], out_dlogits [B, T, V]."""
-    import torch
-    what = "nc_policy_loss"
-    dt, ty, f32 = _act_dtype(what, logits), logits.dtype, torch.float32
-    dev = _current(logits)
-    if logits.dim() != 3:
-        raise NcError(f"{what}: logits are [B, T, V]")
-    B, T, V = shape = tuple(logits.shape)
-    bt, per_token = (B, T), advantages.dim() == 2
-    pz, sz = _take_rows(what, "logits", logits, shape, ty, dev, 2)
-    py = _take(what, "targets", targets, bt, torch.int32, dev)
-    pa = _take(what, "advantages", advantages, bt if per_token else (B,), f32, dev)
-    ps = _take(what, "out_stats", out_stats, (3,), f32, dev)
-    pl = _take(what, "out_logp", out_logp, bt, f32, dev)
-    po = None if old_logp is None else _take(what, "old_logp", old_logp, bt, f32, dev)
-    pr = None if ref_logp is None else _take(what, "ref_logp", ref_logp, bt, f32, dev)
-    ldl, pd, lddl = _even_rows(what, "logits", sz, B, T, V), None, 0
-    if out_dlogits is not None:
-        pd, sd = _take_rows(what, "out_dlogits", out_dlogits, shape, ty, dev, 2)
-        lddl = _even_rows(what, "out_dlogits", sd, B, T, V)
-    workspace, pw, nbytes = _scratch(workspace, _policy_bytes(), logits)
-    rc = lib().nc_policy_loss(pz, ldl, py, pa, per_token, po, pr, B, T, V, clip_low, clip_high, kl_beta, norm, ps, pl, pd, lddl,
-                              dt, pw, nbytes, _raw_stream(stream, dev))
-    if rc:
-        _check(rc, what)
-
-
-@functools.lru_cache(maxsize=1)
-def _policy_bytes() -> int:
-    return int(lib().nc_policy_loss_workspace_bytes())
+    (_ncpy or _native()).policy_loss(logits, targets, advantages, out_stats, out_logp, out_dlogits, old_logp, ref_logp,
+                                     clip_low, clip_high, kl_beta, norm, workspace, stream)
 
 
 def nc_get_status(stream=None) -> tuple[int, int]:

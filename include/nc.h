@@ -337,7 +337,10 @@ int nc_prefix_ce(const float* x, const void* w_u, const int32_t* targets, float*
  * ([Math] §QK-Norm with Sharpening, §Rotary Position Embeddings): for every
  * token n and head,
  *   qhat = alpha R(positions[n]) q / sqrt(mean(q^2) + eps),
- * likewise khat, with R the half-split rotation by position * rope_base^(-2i/D).
+ * likewise khat, with R the half-split rotation of nc_forward and nc_attention,
+ *   R u = (u1 cos + u2 sin, -u1 sin + u2 cos), angles position * rope_base^(-2i/D),
+ * or with the angles negated (reverse = 1), as weights trained with
+ * (u1 cos - u2 sin, u2 cos + u1 sin) need.
  * One pass over q, k and v.  The tensors are rows of one token each, given by a
  * pointer and a row stride in elements (so q, k and v may be slices of one
  * projection's output):
@@ -354,11 +357,12 @@ int nc_prefix_ce(const float* x, const void* w_u, const int32_t* targets, float*
  * word.  NC_ERR_SHAPE: D != 128, H % H_kv != 0, N < 0, a stride below its row's
  * width, out_rows < N without slots.  NC_ERR_ALIGN: pointers not 16-byte
  * aligned or strides not a multiple of 16 bytes.  NC_ERR_ARG: a missing
- * pointer, alpha <= 0, rope_base < 1, eps < 0.  N == 0 does nothing. */
+ * pointer, alpha <= 0, rope_base < 1, eps < 0, reverse not 0 or 1.  N == 0 does
+ * nothing. */
 int nc_qk_norm_rope(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
                     const int32_t* positions, const int32_t* slots, int N, int H, int Hkv, int D, void* q_out,
                     long long ldqo, void* k_out, long long ldko, void* v_out, long long ldvo, long long out_rows,
-                    float alpha, float rope_base, float eps, int dtype, void* stream);
+                    float alpha, float rope_base, int reverse, float eps, int dtype, void* stream);
 
 /* Gradient of nc_qk_norm_rope: from q, k (its inputs), positions and the
  * gradients dq_hat [N, H, D], dk_hat [N, H_kv, D] of qhat and khat (row n =
@@ -371,7 +375,7 @@ int nc_qk_norm_rope(const void* q, long long ldq, const void* k, long long ldk, 
 int nc_qk_norm_rope_backward(const void* q, long long ldq, const void* k, long long ldk, const int32_t* positions,
                              const void* dq_hat, long long ldgq, const void* dk_hat, long long ldgk, int N, int H,
                              int Hkv, int D, void* out_dq, long long lddq, void* out_dk, long long lddk, float alpha,
-                             float rope_base, float eps, int dtype, void* stream);
+                             float rope_base, int reverse, float eps, int dtype, void* stream);
 
 /* Attention of B rows in G groups of B / G consecutive rows, the rows of a group
  * sharing a prefix (many samples of one prompt): row b sees the prefix_lens[g]
@@ -399,8 +403,8 @@ int nc_qk_norm_rope_backward(const void* q, long long ldq, const void* k, long l
  * P_max + S_max <= 2^30, strides at least the width they span (NC_ERR_SHAPE);
  * 16-byte aligned pointers, strides multiples of 8 elements (NC_ERR_ALIGN);
  * softmax_scale > 0 and finite (NC_ERR_ARG); a workspace of
- * nc_prefix_attention_workspace_bytes (0 for sizes that need none, or invalid
- * ones), NC_ERR_WORKSPACE otherwise. */
+ * nc_prefix_attention_workspace_bytes (0 on invalid sizes), NC_ERR_WORKSPACE
+ * otherwise.  Lengths must not change while the call runs. */
 size_t nc_prefix_attention_workspace_bytes(int B, int G, int Tq, int H, int Hkv, int P_max, int S_max, int window);
 int nc_prefix_attention(const void* q, long long ldq, const void* k_prefix, const void* v_prefix, long long ldp,
                         long long lsp, const int32_t* prefix_lens, const void* k_suffix, const void* v_suffix,

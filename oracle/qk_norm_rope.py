@@ -6,7 +6,8 @@ only the test suite may import it, and nothing here is shared with the CUDA
 kernels.
 
 Written from "The Mathematics of Karpathy's nanochat": §Rotary Position
-Embeddings (half split, theta_i = base^(-2i/D)) and §QK-Norm with Sharpening:
+Embeddings (half split, RoPE(u) = (u1 cos + u2 sin, -u1 sin + u2 cos) with angle
+t base^(-2i/D); `reverse` negates the angles) and §QK-Norm with Sharpening:
     y = alpha RoPE(x) / sqrt(mean(RoPE(x)^2) + eps).
 The gradient is the vector-Jacobian product of these two steps, each with its
 own Jacobian, last step first.
@@ -23,24 +24,24 @@ def _angles(positions, D, base):
     return np.asarray(positions, F64)[:, None] * theta          # [N, D/2]
 
 
-def rope(x, positions, base: float, inverse: bool = False):
+def rope(x, positions, base: float, reverse: bool = False):
     x = np.asarray(x, F64)
     a = _angles(positions, x.shape[-1], base)[:, None]
-    c, s = np.cos(a), np.sin(a) * (-1.0 if inverse else 1.0)
+    c, s = np.cos(a), np.sin(a) * (-1.0 if reverse else 1.0)
     lo, hi = np.split(x, 2, axis=-1)
-    return np.concatenate([lo * c - hi * s, hi * c + lo * s], axis=-1)
+    return np.concatenate([lo * c + hi * s, hi * c - lo * s], axis=-1)
 
 
-def forward(x, positions, alpha: float, base: float, eps: float):
+def forward(x, positions, alpha: float, base: float, eps: float, reverse: bool = False):
     """x [N, heads, D] at positions [N]."""
-    r = rope(x, positions, base)
+    r = rope(x, positions, base, reverse)
     return alpha * r / np.sqrt(np.mean(r * r, axis=-1, keepdims=True) + eps)
 
 
-def backward(x, positions, dy, alpha: float, base: float, eps: float):
-    r, dy = rope(x, positions, base), np.asarray(dy, F64)
+def backward(x, positions, dy, alpha: float, base: float, eps: float, reverse: bool = False):
+    r, dy = rope(x, positions, base, reverse), np.asarray(dy, F64)
     D = r.shape[-1]
     rho = np.sqrt(np.mean(r * r, axis=-1, keepdims=True) + eps)
     # d(r / rho) / dr = I / rho - r r^T / (D rho^3)
     dr = alpha * (dy / rho - r * np.sum(r * dy, axis=-1, keepdims=True) / (D * rho ** 3))
-    return rope(dr, positions, base, inverse=True)
+    return rope(dr, positions, base, not reverse)

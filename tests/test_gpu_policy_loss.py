@@ -217,7 +217,7 @@ def test_captured_and_replayed_is_bit_identical():
     import torch
     z, y, old, ref, adv = _case(9, 4, 200, 2001, "fp32")
     t = [_t(a) for a in (z, y, adv, old, ref)]
-    ws = torch.empty(int(nc.lib().nc_policy_loss_workspace_bytes()), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(nc.nc_policy_loss_workspace_bytes(), dtype=torch.uint8, device="cuda")
     new = lambda: (torch.empty(3, device="cuda"), torch.empty(4, 200, device="cuda"), torch.empty_like(t[0]))
     got, want = new(), new()
     call = lambda o: nc.nc_policy_loss(t[0], t[1], t[2], *o, old_logp=t[3], ref_logp=t[4], kl_beta=0.05, workspace=ws)

@@ -102,6 +102,26 @@ def test_forward_packed_projection_into_a_cache(N, H, Hkv, dtype):
     assert np.all(kc[rest] == 7.0) and np.all(vc[rest] == 7.0) and np.all(kc[:, Hkv:] == 7.0) and np.all(vc[:, Hkv:] == 7.0)
 
 
+def test_reverse_turns_the_other_way():
+    import torch
+    rng = np.random.default_rng(9)
+    q, k, pos = _draw(rng, (60, 3, D), "fp32"), _draw(rng, (60, 1, D), "fp32"), _positions(rng, 60)
+    qd, kd, pd = _dev(q, "fp32"), _dev(k, "fp32"), torch.from_numpy(pos.astype(np.int32)).cuda()
+    qo, ko, dq, dk = (torch.empty_like(t) for t in (qd, kd, qd, kd))
+    nc.nc_qk_norm_rope(qd, kd, pd, qo, ko, reverse=True)
+    _close(_host(qo), QK.forward(q, pos, ALPHA, BASE, EPS, reverse=True), "fp32")
+    _close(_host(ko), QK.forward(k, pos, ALPHA, BASE, EPS, reverse=True), "fp32")
+    # (dy = x)
+    nc.nc_qk_norm_rope_backward(qd, kd, pd, qd, kd, dq, dk, reverse=True)
+    _status_ok()
+    for got, x in ((dq, q), (dk, k)):
+        x64 = x.astype(np.float64)
+        ref = QK.backward(x, pos, x, ALPHA, BASE, EPS, reverse=True)
+        rho2 = np.mean(x64 ** 2, -1, keepdims=True) + EPS
+        size = _pair(x64) + np.abs(x64) * np.sum(x64 ** 2, -1, keepdims=True) / (D * rho2)
+        assert np.all(np.abs(_host(got) - ref) <= HALF["fp32"] * np.abs(ref) + 2.0 ** -18 * ALPHA / np.sqrt(rho2) * size)
+
+
 def test_forward_in_place_equals_out_of_place():
     import torch
     rng = np.random.default_rng(5)

@@ -26,6 +26,13 @@ def test_qk_norm_keeps_norm_and_depends_on_distance_only():
     assert np.allclose(s1, s2, atol=1e-8)
 
 
+def test_qk_norm_is_that_of_the_model():
+    x, pos = RNG(5).standard_normal((6, 3, 128)), np.array([0, 1, 2, 77, 2047, 100000])
+    want = O.qk_norm(O.rope(x, pos, 1e5), 1.15, 1e-6)
+    assert np.allclose(QK.forward(x, pos, 1.15, 1e5, 1e-6), want, atol=1e-12)
+    assert np.allclose(QK.rope(QK.rope(x, pos, 1e5), pos, 1e5, reverse=True), x, atol=1e-12)
+
+
 @pytest.mark.parametrize("eps", [0.0, 1e-6, 0.5])
 def test_qk_norm_gradient_against_differences(eps):
     rng = RNG(2)

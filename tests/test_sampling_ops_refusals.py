@@ -21,15 +21,15 @@ def _call(fn, names, defaults, **kw):
     return getattr(nc.lib(), fn)(*[a[n] for n in names])
 
 
-QK_NAMES = "q ldq k ldk v ldv pos slots N H Hkv D qo ldqo ko ldko vo ldvo rows alpha base eps dtype stream".split()
+QK_NAMES = "q ldq k ldk v ldv pos slots N H Hkv D qo ldqo ko ldko vo ldvo rows alpha base reverse eps dtype stream".split()
 QK_BASE = dict(q=P, ldq=512, k=P, ldk=256, v=P, ldv=256, pos=P, slots=None, N=4, H=4, Hkv=2, D=128, qo=P, ldqo=512, ko=P,
-               ldko=256, vo=P, ldvo=256, rows=4, alpha=1.15, base=1e5, eps=1e-6, dtype=0, stream=None)
+               ldko=256, vo=P, ldvo=256, rows=4, alpha=1.15, base=1e5, reverse=0, eps=1e-6, dtype=0, stream=None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), "ARG"), (dict(k=None), "ARG"), (dict(pos=None), "ARG"), (dict(qo=None), "ARG"), (dict(ko=None), "ARG"),
     (dict(v=None), "ARG"), (dict(vo=None), "ARG"), (dict(alpha=0.0), "ARG"), (dict(alpha=NAN), "ARG"), (dict(alpha=INF), "ARG"),
-    (dict(base=0.5), "ARG"), (dict(base=NAN), "ARG"), (dict(eps=-1.0), "ARG"), (dict(eps=NAN), "ARG"), (dict(dtype=2), "ARG"),
+    (dict(base=0.5), "ARG"), (dict(base=NAN), "ARG"), (dict(reverse=2), "ARG"), (dict(eps=-1.0), "ARG"), (dict(eps=NAN), "ARG"), (dict(dtype=2), "ARG"),
     (dict(N=-1), "SHAPE"), (dict(H=0), "SHAPE"), (dict(Hkv=0), "SHAPE"), (dict(Hkv=3), "SHAPE"), (dict(D=64), "SHAPE"),
     (dict(rows=3), "SHAPE"), (dict(rows=-1, slots=P), "SHAPE"), (dict(ldq=504), "SHAPE"), (dict(ldk=248), "SHAPE"),
     (dict(ldv=248), "SHAPE"), (dict(ldqo=504), "SHAPE"), (dict(ldko=248), "SHAPE"), (dict(ldvo=0), "SHAPE"),
@@ -44,9 +44,9 @@ def test_qk_norm_rope_of_no_tokens_is_nothing():
     assert nc.nc_last_launch_count() == 0
 
 
-QB_NAMES = "q ldq k ldk pos gq ldgq gk ldgk N H Hkv D dq lddq dk lddk alpha base eps dtype stream".split()
+QB_NAMES = "q ldq k ldk pos gq ldgq gk ldgk N H Hkv D dq lddq dk lddk alpha base reverse eps dtype stream".split()
 QB_BASE = dict(q=P, ldq=512, k=P, ldk=256, pos=P, gq=P, ldgq=512, gk=P, ldgk=256, N=4, H=4, Hkv=2, D=128, dq=P, lddq=512, dk=P,
-               lddk=256, alpha=1.15, base=1e5, eps=1e-6, dtype=1, stream=None)
+               lddk=256, alpha=1.15, base=1e5, reverse=1, eps=1e-6, dtype=1, stream=None)
 
 
 @pytest.mark.parametrize("kw,status", [
