@@ -292,11 +292,11 @@ def _own(s):
     if c["op"] == "qknorm":
         q_hat = torch.empty(s["q"].shape, dtype=s["q"].dtype, device=s["q"].device)
         nc.nc_qk_norm_rope(s["q"], s["k"], s["positions"], q_hat, s["k_cache"], v=s["v"], v_out=s["v_cache"], slots=s["slots"],
-                           alpha=ALPHA, rope_base=BASE, eps=EPS)
+                           alpha=ALPHA, rope_base=BASE, eps=EPS, reverse=True)
         return [q_hat, s["k_cache"], s["v_cache"]]
     if c["op"] == "qknorm_bwd":
         dq, dk = torch.empty_like(s["dq_hat"]), torch.empty_like(s["dk_hat"])
-        nc.nc_qk_norm_rope_backward(s["q"], s["k"], s["positions"], s["dq_hat"], s["dk_hat"], dq, dk, alpha=ALPHA, rope_base=BASE, eps=EPS)
+        nc.nc_qk_norm_rope_backward(s["q"], s["k"], s["positions"], s["dq_hat"], s["dk_hat"], dq, dk, alpha=ALPHA, rope_base=BASE, eps=EPS, reverse=True)
         return [dq, dk]
     if c["op"] == "prefix":
         out = torch.empty_like(s["q"])
