@@ -474,7 +474,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const
 // bytes at either end are read directly) in chunks of 16 KB, chunk n of the
 // CTA's sequence in slot n % NS.  Pass 1 leaves the row's last NS chunks where
 // they are; pass 2 takes those first and frees them, and then the ones before,
-// which were freed at once and are copied again (from L2).
+// which were freed at once and are copied again (from L2).  CTA c takes the c-th
+// row with a target, the (c + gridDim.x)-th and so on, which the copying warp
+// finds by counting, so that padding leaves all CTAs the same work; between them
+// the others write the zeros of rows without a target.
 constexpr int kChunk = 16384, kMeta = 16;
 template <int CPS> struct Ring {
   static constexpr int NS = CPS == 1 ? 13 : 6, WORK = CPS == 1 ? 512 : 256;  // slots, working threads
@@ -490,7 +493,10 @@ __global__ void __launch_bounds__(Ring<CPS>::WORK + 32, CPS) k_policy_ring(const
   __shared__ uint64_t bars[2 * NS + 2];
   __shared__ Row s_row[2];
   __shared__ float s_top[2];
-  __shared__ double s_part[kMeta];  // norm 1: 1 / tokens of the sequence of the CTA's k-th row, at k % kMeta
+  // of the CTA's k-th row, at k % kMeta: the row (-1: there is none) and its
+  // target, there with its first chunk; norm 1: 1 / its sequence's tokens
+  __shared__ int s_at[kMeta], s_y[kMeta];
+  __shared__ double s_part[kMeta];
   __shared__ double2 s_log[kLogTable];
   __shared__ float s_m[2][kWarps];
   __shared__ double s_s[2][kWarps];
@@ -523,11 +529,7 @@ __global__ void __launch_bounds__(Ring<CPS>::WORK + 32, CPS) k_policy_ring(const
     int n = 0, last_b = -1, k = 0;
     double part_of = 1.0;
     bool ok = true;
-    int y = blockIdx.x < M ? a.targets[blockIdx.x] : -1;
-    for (int row = blockIdx.x; ok && row < M; row += gridDim.x) {
-      const int y_row = y;
-      if (row + (int)gridDim.x < M) y = a.targets[row + gridDim.x];
-      if (!valid(y_row, V)) continue;
+    auto take = [&](int row, int y) {
       const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.ldl;
       const int head = head_of(z, V), nq = (V - head) / N, C = (nq + kVec - 1) / kVec;
       const int again = grad && C > NS ? C - NS : 0;
@@ -535,6 +537,10 @@ __global__ void __launch_bounds__(Ring<CPS>::WORK + 32, CPS) k_policy_ring(const
         const int c = i < C ? i : i - C;
         const uint32_t bytes = (uint32_t)min(kVec, nq - c * kVec) * 16u;
         if (abort_flag || !ptx::mbar_wait(empty(n), ((uint32_t)(n / NS) & 1u) ^ 1u, a.status)) return false;
+        if (i == 0) {
+          s_at[k % kMeta] = row;
+          s_y[k % kMeta] = y;
+        }
         ptx::mbar_arrive_expect_tx(full(n), bytes);
         ptx::bulk_load(ptx::smem_u32(ring + (n % NS) * kChunk), z + head + (size_t)c * kVec * N, bytes, full(n));
         ++n;
@@ -555,6 +561,38 @@ __global__ void __launch_bounds__(Ring<CPS>::WORK + 32, CPS) k_policy_ring(const
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       ++k;
+    };
+    // 128 targets at a time, the next ones on their way
+    constexpr int kScan = 4;
+    int y[kScan], y_next[kScan], before = 0, rank = blockIdx.x;
+    auto load = [&](int base) {
+#pragma unroll
+      for (int i = 0; i < kScan; ++i) y_next[i] = base + 32 * i + lane < M ? a.targets[base + 32 * i + lane] : -1;
+    };
+    load(0);
+    for (int base = 0; ok && base < M; base += 32 * kScan) {
+#pragma unroll
+      for (int i = 0; i < kScan; ++i) y[i] = y_next[i];
+      if (base < M - 32 * kScan) load(base + 32 * kScan);
+#pragma unroll
+      for (int i = 0; i < kScan; ++i) {
+        const unsigned has = __ballot_sync(0xffffffffu, valid(y[i], V));
+        const int mine = before + __popc(has & ((1u << lane) - 1u));
+        while (ok && rank < before + __popc(has)) {
+          const int src = __ffs((int)__ballot_sync(0xffffffffu, ((has >> lane) & 1u) != 0u && mine == rank)) - 1;
+          take(base + 32 * i + src, __shfl_sync(0xffffffffu, y[i], src));
+          rank += gridDim.x;
+        }
+        before += __popc(has);
+      }
+    }
+    if (lane == 0 && ok) {  // no more rows
+      ok = !abort_flag && ptx::mbar_wait(empty(n), ((uint32_t)(n / NS) & 1u) ^ 1u, a.status);
+      if (ok) {
+        s_at[k % kMeta] = -1;
+        ptx::mbar_arrive(full(n));
+        ++n;
+      }
     }
     if (lane == 0) {
       if (!ok) abort_flag = 1;
@@ -571,21 +609,30 @@ __global__ void __launch_bounds__(Ring<CPS>::WORK + 32, CPS) k_policy_ring(const
     const int count = *(volatile int*)&s_count;
     double sum_loss = 0.0, sum_kl = 0.0, sum_clip = 0.0;
     int n = 0, k = 0;  // chunks and rows done
-    int y_next = blockIdx.x < M ? a.targets[blockIdx.x] : -1;
     const double w_all = count > 0 ? 1.0 / count : 0.0;
-    for (int row = blockIdx.x; ok && row < M; row += gridDim.x) {
+    auto wait_full = [&](int i) -> bool { return !abort_flag && ptx::mbar_wait(full(i), (uint32_t)(i / NS) & 1u, a.status); };
+    // the zeros of rows without a target: the CTA's next row to look at
+    int look = blockIdx.x, y_look = look < M ? a.targets[look] : -1;
+    auto look_at_one = [&] {
+      const int row = look, y = y_look;
+      look += gridDim.x;
+      y_look = look < M ? a.targets[look] : -1;
+      if (valid(y, V)) return;
+      if (tid == 0) {
+        a.out_logp[row] = 0.f;
+        if (y != -1) atomicOr(a.status, kStatusData);  // a bad target: recorded, and the token counts as padding
+      }
+      if (grad) zero_row(static_cast<T*>(a.dlogits) + (size_t)row * a.lddl, V, tid, kWork);
+    };
+    while (ok) {
+      if (!wait_full(n)) {
+        ok = false;
+        break;
+      }
+      const int row = s_at[k % kMeta], y = s_y[k % kMeta];
+      if (row < 0) break;
       const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.ldl;
       T* dz = static_cast<T*>(a.dlogits) + (size_t)row * a.lddl;
-      const int y = y_next;
-      if (row + (int)gridDim.x < M) y_next = a.targets[row + gridDim.x];  // on its way during this row
-      if (!valid(y, V)) {
-        if (tid == 0) {
-          a.out_logp[row] = 0.f;
-          if (y != -1) atomicOr(a.status, kStatusData);
-        }
-        if (grad) zero_row(dz, V, tid, kWork);
-        continue;
-      }
       T zy = T(0.f);
       float adv = 0.f, old = 0.f, ref = 0.f;
       if (tid == 0) {  // on their way while the row is summed
@@ -604,7 +651,6 @@ __global__ void __launch_bounds__(Ring<CPS>::WORK + 32, CPS) k_policy_ring(const
         ze = Act<T>::ld(z + edge);
         o.add1(ze);
       }
-      auto wait_full = [&](int i) -> bool { return !abort_flag && ptx::mbar_wait(full(i), (uint32_t)(i / NS) & 1u, a.status); };
       auto release = [&](int i) {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(empty(i));
@@ -702,7 +748,9 @@ __global__ void __launch_bounds__(Ring<CPS>::WORK + 32, CPS) k_policy_ring(const
       }
       n += C + again;
       ++k;
+      if (look < M) look_at_one();
     }
+    while (ok && look < M) look_at_one();
     if (!ok) abort_flag = 1;
     if (tid == 0) {
       part[3 * blockIdx.x] = sum_loss;
