@@ -760,13 +760,19 @@ __global__ void __launch_bounds__(Ring<CPS>::WORK + 32, CPS) k_policy_ring(const
   }
 }
 
-// the CTAs' sums in a fixed order, one warp per statistic
+// the CTAs' sums in a fixed order, one warp per statistic, eight loads in flight
 __global__ void __launch_bounds__(96) k_policy_stats(const double* part, int n, float* out) {
   pdl_launch_dependents();
   pdl_wait();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double s = 0.0;
-  for (int i = lane; i < n; i += 32) s += part[3 * i + w];
+  for (int i0 = lane; i0 < n; i0 += 256) {
+    double v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = i0 + 32 * k < n ? part[3 * (i0 + 32 * k) + w] : 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += v[k];
+  }
   s = warp_sum_d(s);
   if (lane == 0) out[w] = (float)s;
 }
