@@ -815,11 +815,11 @@ static int run(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) 
   if (bytes <= 8192) return run_warp<T>(a, part, num_sms, st);
   if (bytes <= 32768) return run_rows<T, 256>(a, part, num_sms, st);
   // two CTAs per SM overlap one row's sums with the other's writes, unless much
-  // of a row does not fit half the memory and is copied twice (8192 rows: 32768
-  // words 337 us against 361 with one CTA, 60000 words of 4096 rows 375 against
-  // 310); up to a row per SM, one CTA with twice the threads has it sooner
-  // (64 rows of 32768 words: 9.9 us against 12.3)
-  if (bytes <= 147456 && M > num_sms) return run_ring<T, 2>(a, part, num_sms, st);
+  // of a row does not fit half the memory and is copied twice (fp32, 8192 rows:
+  // 32768 words 324 us against 364 with one CTA, 40000 words 403 against 420;
+  // 4096 rows of 60000 words 359 against 308); up to a row per SM, one CTA with
+  // twice the threads has it sooner (64 rows of 32768 words: 9.9 us against 12.3)
+  if (bytes <= 184320 && M > num_sms) return run_ring<T, 2>(a, part, num_sms, st);
   return run_ring<T, 1>(a, part, num_sms, st);
 }
 
