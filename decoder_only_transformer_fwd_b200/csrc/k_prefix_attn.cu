@@ -321,17 +321,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // Tensor memory first: the second CTA of an SM starts only when the first has
-  // given up its allocation permit (measured: 2.6 us after it with the
-  // allocation behind the tables of starts, 0.6 us with it here).  The next
-  // kernel may start only after that, so that nothing that waits for this one
-  // holds tensor memory that it still needs.
-  if (warp == kWarpMma) {
-    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
-    ptx::tmem_relinquish();
-    ptx::tc_fence_before();
-    pdl_launch_dependents();
-  }
   if (threadIdx.x == 0) {
     ptx::mbar_init(bar(B_QF), 1);
     ptx::mbar_init(bar(B_QE), 1);
@@ -358,6 +347,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kWarpTma && lane < 6)
     ptx::prefetch_tmap(lane == 0 ? &tmQp : lane == 1 ? &tmQs : lane == 2 ? &tmKp : lane == 3 ? &tmVp : lane == 4 ? &tmKs : &tmVs);
   pdl_wait();  // lengths, q and the caches may come from the previous kernel
+  // Tensor memory before anything else: the second CTA of an SM starts only when
+  // the first has given up its allocation permit (measured: 2.6 us after it with
+  // the allocation behind the tables, 0.6 us with it ahead of them).  It comes
+  // after the wait, and the next kernel may start only after it: a CTA that holds
+  // tensor memory never waits for a kernel that may still need some.
+  if (warp == kWarpMma) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+    pdl_launch_dependents();
+  }
   fill_tables(a, start, seen, warp, lane);
   const int bins = a.bins_p + a.bins_s, total = start[bins];
   const int share = share_of(a, total);

@@ -79,6 +79,8 @@ def _run(q, kp, vp, pl, ks, vs, sl, window=0, scale=None):
     (2, 2, 2, 2, 1, [0, 40], [0, 0], 0),                             # a row without any key
     (3, 1, 1, 2, 2, [500], [10, 200, 0], 64),                        # window: prefix seen in part, not at all, at its end
     (3, 1, 4, 2, 2, [500], [10, 200, 0], 1),                         # each query sees itself alone
+    (3, 1, 2, 4, 2, [0], [0, 0, 0], 0),                              # no keys at all
+    (3, 1, 2, 4, 2, [0], [0, 0, 0], 5),
     (2, 1, 130, 1, 1, [70], [130, 200], 0),                          # several query tiles per row
     (2, 1, 130, 2, 1, [70], [131, 190], 50),
     (40, 1, 1, 12, 3, [333], [0] * 20 + list(range(1, 21)), 0),      # 160 query rows per key head: two tiles
