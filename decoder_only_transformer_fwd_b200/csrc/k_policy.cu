@@ -16,10 +16,10 @@
 // HBM bound: the logits in once, the gradient out once (2 V elements per
 // token).  Three forms, by a row's bytes:
 //   k_policy_warp  rows up to 8 KB: a warp takes a row at a time;
-//   k_policy_loss  rows up to 32 KB: a CTA of 256 threads takes a row at a time.
-//     Both make one pass with a running maximum and sum, then a second one that
-//     reads the row again (from L2, where the first left it) and writes the
-//     gradient.  Several rows per SM cover each other's latencies.
+//   k_policy_rows  rows up to 20 KB (fp32) or 40 KB (bf16): a CTA takes a row at a
+//     time.  Both make one pass with a running maximum and sum, then a second one
+//     that reads the row again (from L2, where the first left it) and writes the
+//     gradient.  Many rows per SM cover each other's latencies.
 //   k_policy_ring  longer rows: bulk copies bring a row into a shared-memory
 //     ring, both passes read it there, and the next row's copies run meanwhile.
 #include <cfloat>
@@ -393,8 +393,9 @@ __global__ void __launch_bounds__(32 * kWarpRows, kWarpCtas) k_policy_warp(const
   }
 }
 
+constexpr int kRowThreads = 1280;  // per SM
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const PolicyArgs a, double* part) {
+__global__ void __launch_bounds__(kThreads, kRowThreads / kThreads) k_policy_rows(const PolicyArgs a, double* part) {
   __shared__ float s_m[kThreads / 32];
   __shared__ double s_s[kThreads / 32];
   __shared__ Row s_row;
@@ -480,7 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_policy_loss(const
 // the others write the zeros of rows without a target.
 constexpr int kChunk = 16384, kMeta = 16;
 template <int CPS> struct Ring {
-  static constexpr int NS = CPS == 1 ? 13 : 6, WORK = CPS == 1 ? 512 : 256;  // slots, working threads
+  static constexpr int NS = CPS == 1 ? 13 : CPS == 2 ? 6 : 3;             // slots
+  static constexpr int WORK = CPS == 1 ? 512 : CPS == 2 ? 256 : 128;      // working threads
   static constexpr int SMEM = NS * kChunk + 1024;
 };
 
@@ -782,9 +784,9 @@ __global__ void __launch_bounds__(96) k_policy_stats(const double* part, int n, 
 template <typename T, int THREADS>
 static int run_rows(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
   const int M = a.B * a.T;
-  int grid = num_sms * (1024 / THREADS) < kPolicyMaxCtas ? num_sms * (1024 / THREADS) : kPolicyMaxCtas;
+  int grid = num_sms * (kRowThreads / THREADS) < kPolicyMaxCtas ? num_sms * (kRowThreads / THREADS) : kPolicyMaxCtas;
   if (grid > M) grid = M;
-  launch_pdl(k_policy_loss<T, THREADS>, dim3(grid), dim3(THREADS), 0, st, 1, a, part);
+  launch_pdl(k_policy_rows<T, THREADS>, dim3(grid), dim3(THREADS), 0, st, 1, a, part);
   return grid;
 }
 
@@ -810,17 +812,29 @@ template <typename T>
 static int run(const PolicyArgs& a, double* part, int num_sms, cudaStream_t st) {
   const size_t bytes = (size_t)a.V * sizeof(T);
   const int M = a.B * a.T;
-  // measured, fp32, 16384 rows: 2048 words 96 us with a CTA of 256 threads per
-  // row, 56 us with a warp; 8192 words 191 us against 198 with 128 threads
+  // Up to a row per SM, more threads have it sooner (64 rows of 32768 fp32 words:
+  // 9.9 us with 512, 12.3 with 256; 100 rows of 20000 bf16 words 7.9 with 512,
+  // 11.3 with 128).
+  // Beyond, measured in us with gradient, three quarters of the rows with a target:
+  //   fp32, 16384 rows: 2048 words 56 with a warp per row, 60 with a CTA of 128
+  //   threads; 2500 words 82 against 73; 5000 words 122 against 125 with the ring;
+  //   8192 rows: 6500 words 90 against 74; 9000 words 103 with four CTAs per SM on
+  //   the ring, 116 with two; 12000 words 125 against 131; 20000 words 196 with two.
+  //   bf16: 16384 rows of 5000 words 80 with a CTA of 128 threads, 99 with a warp;
+  //   8192 rows: 17000 words 125 against 141 with the ring; 24000 words 194 against 163.
+  const bool few = M <= num_sms;
   if (bytes <= 8192) return run_warp<T>(a, part, num_sms, st);
-  if (bytes <= 32768) return run_rows<T, 256>(a, part, num_sms, st);
+  if (bytes <= (sizeof(T) == 4 ? 20480 : 40960))
+    return few ? run_rows<T, 512>(a, part, num_sms, st) : run_rows<T, 128>(a, part, num_sms, st);
+  if (few) return run_ring<T, 1>(a, part, num_sms, st);
+  if constexpr (sizeof(T) == 4) {
+    if (bytes <= 49152) return run_ring<T, 4>(a, part, num_sms, st);
+  }
   // two CTAs per SM overlap one row's sums with the other's writes, unless much
   // of a row does not fit half the memory and is copied twice (fp32, 8192 rows:
-  // 32768 words 324 us against 364 with one CTA, 40000 words 403 against 420;
-  // 4096 rows of 60000 words 359 against 308); up to a row per SM, one CTA with
-  // twice the threads has it sooner (64 rows of 32768 words: 9.9 us against 12.3)
-  if (bytes <= 184320 && M > num_sms) return run_ring<T, 2>(a, part, num_sms, st);
-  return run_ring<T, 1>(a, part, num_sms, st);
+  // 32768 words 324 against 364 with one CTA, 40000 words 403 against 420; 4096
+  // rows of 60000 words 359 against 308)
+  return bytes <= 184320 ? run_ring<T, 2>(a, part, num_sms, st) : run_ring<T, 1>(a, part, num_sms, st);
 }
 
 bool launch_policy_loss(const PolicyArgs& a, int act_bf16, double* part, int num_sms, cudaStream_t st) {

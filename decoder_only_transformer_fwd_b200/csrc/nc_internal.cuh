@@ -251,7 +251,7 @@ bool launch_prefix_attn(const PrefixAttnArgs& a, const void* q, long long ldq, c
                         void* workspace, cudaStream_t st);
 
 // Clipped policy loss (k_policy.cu); part: 3 doubles per CTA.
-constexpr int kPolicyMaxCtas = 1024;
+constexpr int kPolicyMaxCtas = 2048;
 struct PolicyArgs {
   const void* logits;
   long long ldl;

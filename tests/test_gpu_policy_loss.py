@@ -2,9 +2,10 @@
 (oracle/policy_loss.py).
 
 Tolerance.  A weight exp(z - max) is off by 2^-22 (the exponential) and by
-2^-24 times its argument (at most 2^-19 where it counts: e^-x x < 0.37), and a
-thread adds up at most ceil(V / 512) + 8 of them in fp32; what lies across
-threads, the logarithm and the ratio are fp64.  For V <= 41000 that is below
+2^-24 times its argument (at most 2^-19 where it counts: e^-x x < 0.37), and
+passes through at most 50 roundings of a thread's sum in fp32 (words of a
+chunk first, then the chunks); what lies across threads and the logarithm are
+fp64.  Together that is below
 2^-17 relative, so lp is off by at most 2^-17 + 2^-24 |lp|.  The ratio and the
 KL term follow lp: dL/dlp is off by at most 2^-16 of its terms' size, a
 gradient element by 2^-15 of that size times (p + [v = y]), plus half a step of
@@ -95,8 +96,14 @@ def _check(got, want, dtype):
     (1, 5, 32768, "fp32", 0, 0.05, False),
     (1, 3, 40009, "fp32", 1, 0.05, False),
     (1, 3, 40009, "bf16", 0, 0.05, False),
-    (2, 2, 8193, "fp32", 0, 0.05, True),                     # the first sizes beyond 32 KB a row
+    (2, 2, 8193, "fp32", 0, 0.05, True),
     (2, 2, 16391, "bf16", 1, 0.05, True),
+    (2, 3, 5121, "fp32", 0, 0.05, True),                     # the borders of 20 and 40 KB a row, few rows
+    (2, 3, 20480, "bf16", 1, 0.05, True),
+    (3, 150, 5120, "fp32", 0, 0.05, True),                   # and many
+    (3, 150, 5123, "fp32", 1, 0.05, True),
+    (3, 130, 20479, "bf16", 0, 0.05, True),
+    (3, 130, 12289, "fp32", 0, 0.05, True),                  # the border of 48 KB
     (1, 3, 60001, "fp32", 0, 0.05, False),                   # a row longer than shared memory
     (3, 150, 9001, "fp32", 1, 0.0, False),                   # several long rows per CTA
     (3, 150, 20011, "bf16", 1, 0.05, True),
