@@ -839,7 +839,12 @@ bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes) {
   // the cost of everything and its product with the CTAs' number fit an int
   const long long most = 0x7fffffffLL / 2;
   if (units_p > most || units_s > most) return false;
-  if (units_p * (ceil_div(a->P_max, kKeys) + kUnitCost) + units_s * (ceil_div(a->S_max, kKeys) + kUnitCost) > most) return false;
+  const long long kt_p = ceil_div(a->P_max, kKeys), kt_s = ceil_div(a->S_max, kKeys);
+  const long long cost = units_p * (kt_p + kUnitCost) + units_s * (kt_s + kUnitCost);
+  if (cost > most) return false;
+  // pieces that a row may have with full caches
+  const long long share = ceil_div(cost, a->ctas) > kUnitCost + 1 ? ceil_div(cost, a->ctas) : kUnitCost + 1;
+  a->most_pieces = (int)(kt_p / share + kt_s / share + 2);
   auto align = [](size_t b) { return (b + 255) & ~size_t(255); };
   const size_t rows_p = units_p > 0 ? (size_t)(units_p + a->ctas) * (a->box_p * R) : 0;  // a slot per unit and CTA
   const size_t rows_s = units_s > 0 ? (size_t)(units_s + a->ctas) * (a->box_s * R) : 0;
@@ -878,9 +883,10 @@ bool launch_prefix_attn(const PrefixAttnArgs& args, const void* q, long long ldq
   }
   const long long rows = (long long)tokens * a.H;
   LaunchScope scope_(KK_PREFIX_ATTN, st);
-  // few rows: their pieces are spread over sixteen warps, or four (12 rows of 171
-  // pieces: 17.2 us for the whole call with four, 13.6 with sixteen)
-  if (rows <= 148) return launch_pdl(k_prefix_combine<16>, dim3((unsigned)rows), dim3(512), 0, st, 1, a) == cudaSuccess;
+  // Few rows: their pieces are spread over four warps, or, where there may be
+  // many, over sixteen (12 rows of 171 pieces: 17.2 us for the whole call with
+  // four, 13.6 with sixteen; 48 rows of up to 5 pieces: 10.7 against 11.4).
+  if (rows <= 148 && a.most_pieces > 32) return launch_pdl(k_prefix_combine<16>, dim3((unsigned)rows), dim3(512), 0, st, 1, a) == cudaSuccess;
   if (rows <= kPrefixSplitRows) return launch_pdl(k_prefix_combine<4>, dim3((unsigned)rows), dim3(128), 0, st, 1, a) == cudaSuccess;
   return launch_pdl(k_prefix_combine<1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, a) == cudaSuccess;
 }

@@ -87,6 +87,7 @@ def _run(q, kp, vp, pl, ks, vs, sl, window=0, scale=None):
     (2, 1, 1, 128, 1, [100], [3, 9], 0),                             # 128 query heads on one key head
     (6, 3, 1, 96, 2, [100, 1, 64], [3, 9, 0, 1, 2, 64], 0),          # 48 rows per token: two tokens fit a tile
     (5, 1, 2, 4, 4, [3000], [900, 1, 450, 30, 2], 0),                # many splits
+    (1, 1, 1, 12, 1, [9000], [3], 0),                                # a row of some fifty pieces
     (5, 1, 2, 4, 4, [3000], [900, 1, 450, 30, 2], 1000),
 ])
 def test_against_the_definition(B, G, Tq, H, Hkv, pl, sl, window):
@@ -196,13 +197,13 @@ def test_lengths_out_of_range_are_clamped_and_flagged():
         _check(out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64), q, kp, vp, cp, ks, vs, cs, 0, D ** -0.5)
 
 
-def test_agrees_with_the_attention_layer():
+@pytest.mark.parametrize("T,P,H,Hkv,w", [(300, 200, 4, 4, 96), (900, 260, 4, 2, 900), (900, 10, 6, 2, 333)])
+def test_agrees_with_the_attention_layer(T, P, H, Hkv, w):
     """A prompt and its continuation, token by token in the cache, against nc_attention on the joined sequence: both
     round their weights and outputs to bf16, 2^-8 each, of sums of |v| that stay below 5."""
     import torch
     rng = np.random.default_rng(18)
-    T, P, H, w = 300, 200, 4, 96
-    q, k, v = (_dev(_bf(rng, 1, T, H, D)) for _ in range(3))
+    q, k, v = (_dev(_bf(rng, 1, T, h, D)) for h in (H, Hkv, Hkv))
     ref = torch.empty_like(q)
     nc.nc_attention(q, k, v, ref, w, rope_qknorm=0)
     out = torch.empty(1, T - P, H, D, dtype=q.dtype, device="cuda")
