@@ -747,7 +747,8 @@ __global__ void __launch_bounds__(WPR > 4 ? 32 * WPR : 128) k_prefix_combine(con
     const float l = p < parts ? *lse : -INFINITY;
     load(0);
     const float m_new = fmaxf(m, warp_max(l));
-    if (m_new == -INFINITY) continue;
+    // (a maximum skips NaN, so a row of nothing else is told apart from an empty one)
+    if (m_new == -INFINITY && !__any_sync(0xffffffffu, l != l)) continue;
     const float w = ex2((l - m_new) * 1.4426950408889634f), old = ex2((m - m_new) * 1.4426950408889634f);
     m = m_new;
     sum = sum * old + warp_sum(w);
@@ -773,7 +774,7 @@ __global__ void __launch_bounds__(WPR > 4 ? 32 * WPR : 128) k_prefix_combine(con
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < WPR; ++i) {
-      const float w = s_m[i] == -INFINITY ? 0.f : ex2((s_m[i] - top) * 1.4426950408889634f);
+      const float w = s_sum[i] == 0.f ? 0.f : ex2((s_m[i] - top) * 1.4426950408889634f);
       const float4 x = s_acc[i][lane];
       acc.x += w * x.x, acc.y += w * x.y, acc.z += w * x.z, acc.w += w * x.w;
       sum += w * s_sum[i];

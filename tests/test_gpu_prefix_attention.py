@@ -185,6 +185,40 @@ def test_values_before_every_window_may_be_anything():
     _check(out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64), q, kp, vp, pl, ks, vs, sl, w, D ** -0.5)
 
 
+@pytest.mark.parametrize("B,H,P", [(3, 2, 300), (1, 12, 9000), (400, 8, 70)])  # the three ways pieces are joined
+def test_not_a_number_stays_in_its_row(B, H, P):
+    """A query that is not a number gives a row of NaN, not an empty one; a key
+    that is not one gives NaN in the rows that see it.  The others keep their bits."""
+    import torch
+    q, kp, vp, ks, vs = _inputs(31, B, 1, 1, H, 1, P, 8)
+    sl = [i % 9 for i in range(B)]
+    t, lens = [_dev(x) for x in (kp, vp, ks, vs)], (_i32([P]), _i32(sl))
+
+    def run(qd):
+        out, lse = torch.empty_like(qd), torch.empty(B, 1, H, device="cuda")
+        nc.nc_prefix_attention(qd, t[0], t[1], lens[0], t[2], t[3], lens[1], out, out_lse=lse)
+        torch.cuda.synchronize()
+        assert nc.nc_get_status()[0] == 0
+        return out, lse
+
+    o0, l0 = run(_dev(q))
+    bad = _dev(q)
+    bad[B // 2, 0, 1] = float("nan")
+    hit = torch.zeros(B, 1, H, dtype=torch.bool, device="cuda")
+    hit[B // 2, 0, 1] = True
+    o1, l1 = run(bad)
+    assert torch.isnan(o1[hit]).all() and torch.isnan(l1[hit]).all()
+    assert torch.equal(o1[~hit], o0[~hit]) and torch.equal(l1[~hit], l0[~hit])
+    if B > 1:
+        row = next(b for b in range(B) if sl[b] > 0)
+        t[2][row, 0] = float("nan")
+        hit.zero_()
+        hit[row] = True
+        o2, l2 = run(_dev(q))
+        assert torch.isnan(o2[hit]).all() and torch.isnan(l2[hit]).all()
+        assert torch.equal(o2[~hit], o0[~hit]) and torch.equal(l2[~hit], l0[~hit])
+
+
 def test_lengths_out_of_range_are_clamped_and_flagged():
     import torch
     q, kp, vp, ks, vs = _inputs(17, 2, 1, 1, 2, 2, 70, 30)
