@@ -999,7 +999,7 @@ int nc_policy_loss(const void* logits, long long ldl, const int32_t* targets, co
       !(kl_beta >= 0.f) || !std::isfinite(kl_beta) || (norm != 0 && norm != 1) ||
       (adv_per_token != 0 && adv_per_token != 1) || (dtype != NC_BF16 && dtype != NC_FP32))
     return NC_ERR_ARG;
-  if (B <= 0 || T <= 0 || V <= 0 || (long long)B * T > 0x7fffffffLL || V > (1 << 30) || ldl < V ||
+  if (B <= 0 || T <= 0 || V <= 0 || (long long)B * T > (1 << 30) || V > (1 << 30) || ldl < V ||
       (out_dlogits_opt && lddl < V))
     return NC_ERR_SHAPE;
   const uintptr_t esz = dtype == NC_BF16 ? 2 : 4;  // rows may start anywhere, elements may not

@@ -437,8 +437,9 @@ int nc_prefix_attention(const void* q, long long ldq, const void* k_prefix, cons
  * threads, in a fixed order.  A target outside [-1, V) sets NC_ERR_DATA and
  * counts as -1.  -inf logits have probability 0.  NC_ERR_ARG: a missing
  * pointer, clip_low outside [0, 1), clip_high < 0, kl_beta < 0, norm not 0 or 1;
- * NC_ERR_SHAPE: B, T or V < 1, a stride below V; NC_ERR_ALIGN: rows not aligned
- * to their element, workspace not to 16 bytes; NC_ERR_WORKSPACE. */
+ * NC_ERR_SHAPE: B, T or V < 1, B T or V above 2^30, a stride below V;
+ * NC_ERR_ALIGN: rows not aligned to their element, workspace not to 16 bytes;
+ * NC_ERR_WORKSPACE. */
 size_t nc_policy_loss_workspace_bytes(void);
 int nc_policy_loss(const void* logits, long long ldl, const int32_t* targets, const float* advantages, int adv_per_token,
                    const float* old_logp_opt, const float* ref_logp_opt, int B, int T, int V, float clip_low,

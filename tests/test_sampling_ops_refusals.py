@@ -98,7 +98,7 @@ PL_BASE = dict(z=P, ldl=16, y=P, adv=P, per=0, old=None, ref=None, B=2, T=3, V=1
     (dict(lo=-0.1), "ARG"), (dict(lo=1.0), "ARG"), (dict(lo=NAN), "ARG"), (dict(hi=-0.1), "ARG"), (dict(hi=INF), "ARG"),
     (dict(beta=-1.0), "ARG"), (dict(beta=NAN), "ARG"), (dict(norm=2), "ARG"), (dict(per=2), "ARG"), (dict(dtype=3), "ARG"),
     (dict(B=0), "SHAPE"), (dict(T=0), "SHAPE"), (dict(V=0), "SHAPE"), (dict(ldl=15), "SHAPE"), (dict(lddl=15), "SHAPE"),
-    (dict(B=1 << 16, T=1 << 16), "SHAPE"), (dict(z=OFF2), "ALIGN"), (dict(dz=OFF2), "ALIGN"), (dict(y=OFF2), "ALIGN"),
+    (dict(B=1 << 16, T=1 << 16), "SHAPE"), (dict(B=1 << 15, T=(1 << 15) + 1), "SHAPE"), (dict(z=OFF2), "ALIGN"), (dict(dz=OFF2), "ALIGN"), (dict(y=OFF2), "ALIGN"),
     (dict(adv=OFF2), "ALIGN"), (dict(old=OFF2), "ALIGN"), (dict(ref=OFF2), "ALIGN"), (dict(stats=OFF2), "ALIGN"),
     (dict(logp=OFF2), "ALIGN"), (dict(ws=OFF4), "ALIGN"), (dict(ws=None), "WORKSPACE"), (dict(wsb=100), "WORKSPACE")])
 def test_policy_loss_refuses(kw, status):
