@@ -152,9 +152,10 @@ struct FwdArgs {
 };
 
 // A CTA takes `tok` tokens; its 32 eight-lane groups share them out evenly,
-// and a group walks every (32 / tok)-th head vector of its token with the
-// token's angles in registers, the next vector's load under the current one's
-// arithmetic (and the first one's under the angles').
+// and a group walks every (32 / tok)-th head vector of its token, the next two
+// vectors' loads under the current one's arithmetic (and the first two's under
+// the angles').  With one vector's loads ahead HBM waits: 8192 tokens, 12 + 12
+// heads, bf16, 29.1 us against 26.7.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant__ FwdArgs<T> a) {
   __shared__ __align__(16) float cs[kMaxTok * 2 * kHalf];
@@ -173,8 +174,10 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant
     return hk < 0 ? a.q + n * a.ldq + h * kD : (hv < 0 ? a.k + n * a.ldk + hk * kD : a.v + n * a.ldv + hv * kD);
   };
   int h = group % per;
-  Raw<T> next;
-  if (live && h < a.H + kept) next.load(source(h), j);
+  Raw<T> ahead[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (live && h + i * per < a.H + kept) ahead[i].load(source(h + i * per), j);
   long long slot = live ? (a.slots != nullptr ? (long long)a.slots[n] : (long long)n) : 0;
   fill_angles(a.f, a.positions, a.reverse, n0, ntok, cs, a.status);
   __syncthreads();
@@ -186,10 +189,10 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant
   }
   const uint32_t my_cs = static_cast<uint32_t>(__cvta_generic_to_shared(cs + tl * 2 * kHalf + 8 * j));
   const int heads = a.H + (slot >= 0 ? kept : 0);
-  for (; h < heads; h += per) {
+  auto take = [&](int h, Raw<T>& next) {
     const int hk = h - a.H, hv = hk - a.Hkv;
     Raw<T> raw = next;
-    if (h + per < heads) next.load(source(h + per), j);
+    if (h + 2 * per < heads) next.load(source(h + 2 * per), j);
     T* dst = hk < 0 ? a.qo + n * a.ldqo + h * kD
                     : (hv < 0 ? a.ko + slot * a.ldko + hk * kD : a.vo + slot * a.ldvo + hv * kD);
     if (hv < 0) {
@@ -210,6 +213,14 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant
       raw.set(x);
     }
     raw.store(dst, j);
+  };
+  while (h < heads) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (h >= heads) break;
+      take(h, ahead[i]);
+      h += per;
+    }
   }
 }
 
