@@ -65,10 +65,6 @@ constexpr int kThreads = 192, kWarpTma = 4, kWarpMma = 5;
 constexpr uint32_t TMEM_COLS = 256;        // S0 64 | S1 64 | O 128
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.6931471805599453f;
-// What a unit costs besides its tiles (query load, set-up, rows out), in tiles.
-// 1 against 2 against 3: 8 rows over 32768 keys 43.4, 39.9, 39.8 us; 64 rows over
-// 4096 keys and their own 1024 42.8, 42.8, 44.3 us.
-constexpr int kUnitCost = 2;
 // Query rows up to which a row's pieces are joined by four warps: the CTAs that
 // 148 SMs hold at once.  2048 rows: 29.3 us for the whole call against 30.5 with
 // one warp; 3600 rows: 35.5 against 31.7.
@@ -135,12 +131,14 @@ __device__ __forceinline__ int unit_tiles(const PrefixAttnArgs& a, const Seq& s,
   return lo < hi ? (hi + kKeys - 1) / kKeys - *t0 : 0;
 }
 
-__device__ __forceinline__ int unit_cost(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
+__device__ __forceinline__ int unit_cost(const PrefixAttnArgs& a, int suffix, int tiles) {
+  return tiles > 0 ? tiles + (suffix ? a.fixed_s : a.fixed_p) : 0;
+}
 
 // cost of all query tiles of a row, for one key head
 __device__ __forceinline__ int suffix_cost(const PrefixAttnArgs& a, const Seq& s) {
   int c = 0, t0;
-  for (int tt = 0; tt < a.tiles_s; ++tt) c += unit_cost(unit_tiles(a, s, 1, tt, &t0));
+  for (int tt = 0; tt < a.tiles_s; ++tt) c += unit_cost(a, 1, unit_tiles(a, s, 1, tt, &t0));
   return c;
 }
 
@@ -153,7 +151,7 @@ __device__ void fill_tables(const PrefixAttnArgs& a, int* start, int2* seen, int
     for (int g = i * a.bin_p; g < min(a.G, (i + 1) * a.bin_p); ++g) {
       const int least = windowed(a) ? __reduce_min_sync(0xffffffffu, least_suffix(a, g, lane, 32)) : 0;
       const Seq s = prefix_seq(a, g, least);
-      c += a.band * a.tiles_p * unit_cost(unit_tiles(a, s, 0, 0, &t0));
+      c += a.band * a.tiles_p * unit_cost(a, 0, unit_tiles(a, s, 0, 0, &t0));
       if (lane == 0 && a.bin_p == 1) seen[g] = make_int2(s.lo, s.hi);
     }
     if (lane == 0) start[i] = c;
@@ -198,23 +196,26 @@ __device__ __forceinline__ Seq group_seq(const PrefixAttnArgs& a, const int2* se
 
 // share of a band's total cost that a CTA takes
 __device__ __forceinline__ int share_of(const PrefixAttnArgs& a, int total) {
-  return max((total + a.per_band - 1) / a.per_band, kUnitCost + 1);
+  return max((total + a.per_band - 1) / a.per_band, max(a.fixed_p, a.fixed_s) + 1);
 }
 
-// slot of what CTA `cta` of band b does of the band's unit u
+// Slot of what CTA `cta` of band b does of the band's unit u.
 __device__ __forceinline__ int slot_of(const PrefixAttnArgs& a, int suffix, int b, int u, int cta) {
   return b * ((suffix ? a.B * a.tiles_s : a.G * a.tiles_p) * a.band + a.per_band) + u + cta;
 }
 
 // The piece that holds cost position v, as far as `end`; *next: the position
-// behind it.  A piece may have no tile (it holds only a unit's fixed cost).
+// behind it.  All lanes of a warp.  A piece may have no tile (it holds only a unit's fixed cost).
 // Lengths that change while the kernel runs give wrong pieces, but every loop
 // ends and every index stays in range.
-__device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, const int2* seen, int v, int end, int* next) {
-  int lo = 0, hi = a.bins_p + a.bins_s;  // the last bin that starts at or before v
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (start[mid] <= v) lo = mid; else hi = mid;
+__device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, const int2* seen, int band, int cta, int v, int end,
+                          int lane, int* next) {
+  // the last bin that starts at or before v: the warp looks at 32 places at once
+  const int bins = a.bins_p + a.bins_s, step = (bins + 31) / 32;
+  int lo = step * (__popc(__ballot_sync(0xffffffffu, lane * step < bins && start[lane * step] <= v)) - 1);
+  if (step > 1) {
+    const int i = lo + lane;
+    lo += __popc(__ballot_sync(0xffffffffu, lane < step && i < bins && start[i] <= v)) - 1;
   }
   Piece p;
   p.suffix = lo >= a.bins_p;
@@ -224,12 +225,12 @@ __device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, const int2*
     for (p.seq = lo * a.bin_p;; ++p.seq) {
       s = group_seq(a, seen, p.seq);
       tiles = unit_tiles(a, s, 0, 0, &t0);
-      const int all = a.band * a.tiles_p * unit_cost(tiles);
+      const int all = a.band * a.tiles_p * unit_cost(a, 0, tiles);
       if (at < all || p.seq + 1 >= a.G) break;
       at -= all;
     }
-    const int u = min(at / max(unit_cost(tiles), 1), a.band * a.tiles_p - 1);
-    at -= u * unit_cost(tiles);
+    const int u = min(at / max(unit_cost(a, 0, tiles), 1), a.band * a.tiles_p - 1);
+    at -= u * unit_cost(a, 0, tiles);
     p.hk = u / a.tiles_p;
     tt = u % a.tiles_p;
   } else {
@@ -244,13 +245,13 @@ __device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, const int2*
     at -= p.hk * one;
     for (tt = 0;; ++tt) {
       tiles = unit_tiles(a, s, 1, tt, &t0);
-      if (at < unit_cost(tiles) || tt + 1 >= a.tiles_s) break;
-      at -= unit_cost(tiles);
+      if (at < unit_cost(a, 1, tiles) || tt + 1 >= a.tiles_s) break;
+      at -= unit_cost(a, 1, tiles);
     }
   }
-  const int unit_end = v - at + unit_cost(tiles);
+  const int fixed = p.suffix ? a.fixed_s : a.fixed_p, unit_end = v - at + unit_cost(a, p.suffix, tiles);
   *next = max(v + 1, min(end, unit_end));
-  const int first = max(0, at - kUnitCost), last = *next - (v - at) - kUnitCost;
+  const int first = max(0, at - fixed), last = *next - (v - at) - fixed;
   p.t0 = t0 + first;
   p.nt = min(max(0, last - first), max(0, tiles - first));
   p.lo = s.lo;
@@ -258,9 +259,8 @@ __device__ Piece piece_at(const PrefixAttnArgs& a, const int* start, const int2*
   const int tokens = (p.suffix ? 1 : a.rows_per_group) * a.Tq, box = p.suffix ? a.box_s : a.box_p;
   p.tok0 = p.seq * tokens + tt * box;
   p.ntok = min(box, tokens - tt * box);
-  const int b = blockIdx.x % a.bands;
-  p.slot = slot_of(a, p.suffix, b, (p.seq * a.band + p.hk) * (p.suffix ? a.tiles_s : a.tiles_p) + tt, blockIdx.x / a.bands);
-  p.hk += b * a.band;
+  p.slot = slot_of(a, p.suffix, band, (p.seq * a.band + p.hk) * (p.suffix ? a.tiles_s : a.tiles_p) + tt, cta);
+  p.hk += band * a.band;
   return p;
 }
 
@@ -271,16 +271,16 @@ __device__ int2 unit_pieces(const PrefixAttnArgs& a, const int* start, const int
   const int tiles_q = suffix ? a.tiles_s : a.tiles_p, bin = suffix ? a.bin_s : a.bin_p;
   const int tt = u % tiles_q, hk = u / tiles_q % a.Hkv, seq = u / tiles_q / a.Hkv, i0 = seq / bin * bin;
   const int b = hk / a.band, hb = hk % a.band;  // band, head within it
-  int at = start[(suffix ? a.bins_p : 0) + seq / bin] + kUnitCost, t0, tiles;
+  int at = start[(suffix ? a.bins_p : 0) + seq / bin] + (suffix ? a.fixed_s : a.fixed_p), t0, tiles;
   if (!suffix) {
-    for (int i = i0; i < seq; ++i) at += a.band * a.tiles_p * unit_cost(unit_tiles(a, group_seq(a, seen, i), 0, 0, &t0));
+    for (int i = i0; i < seq; ++i) at += a.band * a.tiles_p * unit_cost(a, 0, unit_tiles(a, group_seq(a, seen, i), 0, 0, &t0));
     tiles = unit_tiles(a, group_seq(a, seen, seq), 0, 0, &t0);
-    at += (hb * a.tiles_p + tt) * unit_cost(tiles);
+    at += (hb * a.tiles_p + tt) * unit_cost(a, 0, tiles);
   } else {
     for (int i = i0; i < seq; ++i) at += a.band * suffix_cost(a, suffix_seq(a, i));
     const Seq s = suffix_seq(a, seq);
     at += hb * suffix_cost(a, s);
-    for (int i = 0; i < tt; ++i) at += unit_cost(unit_tiles(a, s, 1, i, &t0));
+    for (int i = 0; i < tt; ++i) at += unit_cost(a, 1, unit_tiles(a, s, 1, i, &t0));
     tiles = unit_tiles(a, s, 1, tt, &t0);
   }
   if (tiles == 0) return make_int2(0, 0);
@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t bar0 = ptx::smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int band = blockIdx.x % a.bands, cta = blockIdx.x / a.bands;  // band of heads, CTA of the band
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(bar(B_QF), 1);
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   fill_tables(a, start, seen, warp, lane);
   const int bins = a.bins_p + a.bins_s, total = start[bins];
   const int share = share_of(a, total);
-  const long long v_begin = (long long)(blockIdx.x / a.bands) * share;
+  const long long v_begin = (long long)cta * share;
   const bool works = v_begin < total;
   const int v0 = (int)min(v_begin, (long long)total), v1 = (int)min(v_begin + share, (long long)total);
   ptx::tc_fence_after();  // the allocation, before the barriers of fill_tables
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       p.nt = 0;
       while (v < v1 && p.nt == 0) {
         int next;
-        p = piece_at(a, start, seen, v, v1, &next);
+        p = piece_at(a, start, seen, band, cta, v, v1, lane, &next);
         v = next;
       }
       if (lane == 0) {
@@ -532,30 +533,36 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float c = a.scale_log2;
     bool ok = true;
     int sc0 = 0, j0 = 0;
-    for (int n = 0; ok; ++n) {
-      Piece p;
-      if (!piece_wait(n, &p)) {
-        ok = false;
-        break;
-      }
+    const int my_tok = (int)threadIdx.x / R;
+    Piece p, p_next;
+    int lo_next, hi_next;
+    // takes the n-th piece, and the keys [lo, hi) that this thread's row sees of
+    // it, from the side's first key (a thread without a row masks nothing: no one
+    // reads its weights)
+    auto look = [&](int n) -> bool {
+      if (!piece_wait(n, &p_next)) return false;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(B_DE + n % kPieces));
-      if (p.nt == 0) break;
-      const int nrows = p.ntok * R;
-      const bool live = (int)threadIdx.x < nrows, warp_live = warp * 32 < nrows;
-      // keys [lo, hi) that this row sees, from the side's first key
-      // (a thread without a row masks nothing: no one reads its weights)
-      int lo = 0, hi = 0x7fffffff;
-      const int token = p.tok0 + (int)threadIdx.x / R;
-      if (live) {
-        const int b = token / a.Tq;
+      lo_next = 0, hi_next = 0x7fffffff;
+      if ((int)threadIdx.x < p_next.ntok * R && p_next.nt > 0) {
+        const int token = p_next.tok0 + my_tok, b = token / a.Tq;
         const int P = a.P_max > 0 ? clamp_len(a.prefix_lens[b / a.rows_per_group], a.P_max) : 0;
         const int S = a.S_max > 0 ? clamp_len(a.suffix_lens[b], a.S_max) : 0;
-        const int pos = P + S - a.Tq + token % a.Tq, base = p.suffix ? P : 0;
-        lo = max(0, pos - a.window + 1 - base);
-        hi = min(p.suffix ? S : P, pos + 1 - base);
-        if (lo >= hi) lo = hi = 0;
+        const int pos = P + S - a.Tq + token % a.Tq, base = p_next.suffix ? P : 0;
+        lo_next = max(0, pos - a.window + 1 - base);
+        hi_next = min(p_next.suffix ? S : P, pos + 1 - base);
+        if (lo_next >= hi_next) lo_next = hi_next = 0;
       }
+      return true;
+    };
+    p.nt = p.ntok = 0;
+    int lo = 0, hi = 0;
+    // The first turn only takes piece 0: every part of the loop stands in the code
+    // once, since a CTA fetches it cold (a second copy of `look` or of the zeros
+    // below costs 0.2 us of a short call each).
+    for (int n = -1;; ++n) {
+      const int nrows = p.ntok * R;
+      const bool live = (int)threadIdx.x < nrows, warp_live = warp * 32 < nrows;
       float m_run = -INFINITY, l_run = 0.f;
       for (int t = 0; t < p.nt; ++t) {
         const int j = j0 + t;
@@ -655,7 +662,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(B_P + (j & 1)));
       }
-      if (!ok || !ptx::mbar_wait(bar(B_FIN), (uint32_t)n & 1u, a.status)) {
+      // the next piece, while the last product runs
+      if (!ok || !look(n + 1) || (n >= 0 && !ptx::mbar_wait(bar(B_FIN), (uint32_t)n & 1u, a.status))) {
         ok = false;
         break;
       }
@@ -685,9 +693,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(B_OE));
+      if (n >= 0 && lane == 0) ptx::mbar_arrive(bar(B_OE));
       sc0 += 2 * p.nt;
       j0 += p.nt;
+      if (p_next.nt == 0) break;
+      p = p_next, lo = lo_next, hi = hi_next;
     }
     if (!ok) *abort_flag = 1;
   }
@@ -789,6 +799,13 @@ __global__ void __launch_bounds__(WPR > 4 ? 32 * WPR : 128) k_prefix_combine(con
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
+// What a unit of so many query rows costs besides its tiles (query load, set-up,
+// rows out), in tiles of about 1 us: 2, 3 or 4.  Against 2 for every unit: 3 x 20
+// rows x 5 queries (126 and 15 rows) over 5000 + 333 keys 27.7 us for 28.8, 4 x
+// 32 rows (128 and 4) over 2000 + 500 40.1 for 41.2.  Against 3 and 4: 64 rows over
+// 4096 + 1024 keys (64 and 1) 43.2 for 44.6, 4 rows over 512 + 64 10.5 for 10.9.
+int unit_fixed(int rows) { return 2 + (rows > 8) + (rows > 64); }
+
 // q [tokens, H, 128] with row stride ldq: box of R heads x box_tok tokens x 64 columns
 bool q_map(CUtensorMap* m, const void* q, long long ldq, int tokens, int H, int R, int box_tok) {
   const uint64_t dims[4] = {kD, (uint64_t)H, (uint64_t)tokens, 1};
@@ -841,10 +858,13 @@ bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes) {
   const long long most = 0x7fffffffLL / 2;
   if (units_p > most || units_s > most) return false;
   const long long kt_p = ceil_div(a->P_max, kKeys), kt_s = ceil_div(a->S_max, kKeys);
-  const long long cost = units_p * (kt_p + kUnitCost) + units_s * (kt_s + kUnitCost);
+  a->fixed_p = unit_fixed(a->box_p * R);
+  a->fixed_s = unit_fixed(a->box_s * R);
+  const long long cost = units_p * (kt_p + a->fixed_p) + units_s * (kt_s + a->fixed_s);
   if (cost > most) return false;
   // pieces that a row may have with full caches
-  const long long share = ceil_div(cost, a->ctas) > kUnitCost + 1 ? ceil_div(cost, a->ctas) : kUnitCost + 1;
+  const long long least = (a->fixed_p > a->fixed_s ? a->fixed_p : a->fixed_s) + 1;
+  const long long share = ceil_div(cost, a->ctas) > least ? ceil_div(cost, a->ctas) : least;
   a->most_pieces = (int)(kt_p / share + kt_s / share + 2);
   auto align = [](size_t b) { return (b + 255) & ~size_t(255); };
   const size_t rows_p = units_p > 0 ? (size_t)(units_p + a->ctas) * (a->box_p * R) : 0;  // a slot per unit and CTA
