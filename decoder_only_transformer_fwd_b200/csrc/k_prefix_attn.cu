@@ -65,11 +65,6 @@ constexpr int kThreads = 192, kWarpTma = 4, kWarpMma = 5;
 constexpr uint32_t TMEM_COLS = 256;        // S0 64 | S1 64 | O 128
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.6931471805599453f;
-// Query rows up to which a row's pieces are joined by four warps: the CTAs that
-// 148 SMs hold at once.  2048 rows: 29.3 us for the whole call against 30.5 with
-// one warp; 3600 rows: 35.5 against 31.7.
-constexpr int kPrefixSplitRows = 148 * 16;
-
 struct Piece {
   int suffix, seq, hk;  // side, group or row, key head
   int tok0, ntok;       // query tokens (token = row * Tq + i)
@@ -904,11 +899,15 @@ bool launch_prefix_attn(const PrefixAttnArgs& args, const void* q, long long ldq
   }
   const long long rows = (long long)tokens * a.H;
   LaunchScope scope_(KK_PREFIX_ATTN, st);
-  // Few rows: their pieces are spread over four warps, or, where there may be
-  // many, over sixteen (12 rows of 171 pieces: 17.2 us for the whole call with
-  // four, 13.6 with sixteen; 48 rows of up to 5 pieces: 10.7 against 11.4).
+  // A row's pieces are joined by one warp, by four where rows are few or may have
+  // many pieces and 148 SMs hold all rows' CTAs at once, by sixteen where both.
+  // Measured in us for the whole call, (rows, pieces at most), one against four
+  // warps: (192, 5) 16.2, 15.5; (384, 7) 19.0, 18.5; (512, 6) 13.7, 14.4; (1152, 4)
+  // 31.9, 33.2; (768, 9) 69.6, 69.1; (768, 12) 18.4, 18.7; (1280, 20) 29.4, 28.1;
+  // (2048, 6) 27.0, 27.7; (3600, 9) 27.8, 32.1.
+  // Four against sixteen: (12, 171) 16.1, 13.6; (48, 4) 10.7, 11.4.
   if (rows <= 148 && a.most_pieces > 32) return launch_pdl(k_prefix_combine<16>, dim3((unsigned)rows), dim3(512), 0, st, 1, a) == cudaSuccess;
-  if (rows <= kPrefixSplitRows) return launch_pdl(k_prefix_combine<4>, dim3((unsigned)rows), dim3(128), 0, st, 1, a) == cudaSuccess;
+  if (rows <= 3 * 148 || (a.most_pieces > 8 && rows <= 16 * 148)) return launch_pdl(k_prefix_combine<4>, dim3((unsigned)rows), dim3(128), 0, st, 1, a) == cudaSuccess;
   return launch_pdl(k_prefix_combine<1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, a) == cudaSuccess;
 }
 
