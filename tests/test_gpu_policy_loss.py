@@ -153,8 +153,8 @@ def test_loss_alone_equals_the_loss_with_gradient(V):
 
 def test_gradient_in_the_place_of_the_logits():
     import torch
-    for dtype, td, V in (("fp32", torch.float32, 1003), ("bf16", torch.bfloat16, 1003), ("fp32", torch.float32, 9001),
-                         ("fp32", torch.float32, 60001)):
+    for dtype, td, V in (("fp32", torch.float32, 1003), ("bf16", torch.bfloat16, 1003), ("fp32", torch.float32, 4099),
+                         ("bf16", torch.bfloat16, 12001), ("fp32", torch.float32, 9001), ("fp32", torch.float32, 60001)):
         z, y, old, _, adv = _case(4, 2, 40 if V < 2000 else 4, V, dtype)
         want = _run(z, y, adv, old, None, dtype, 0.2, 0.28, 0.0, 0)
         zd, stats, logp = _t(z, td), torch.empty(3, device="cuda"), torch.empty(y.shape, device="cuda")
