@@ -65,6 +65,10 @@ constexpr int kThreads = 192, kWarpTma = 4, kWarpMma = 5;
 constexpr uint32_t TMEM_COLS = 256;        // S0 64 | S1 64 | O 128
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.6931471805599453f;
+// The workspace may start at any 16-byte boundary; rows of pieces are stored 32
+// bytes at a time, so the areas in it start at the next multiple of this.
+constexpr size_t kWsAlign = 256;
+
 struct Piece {
   int suffix, seq, hk;  // side, group or row, key head
   int tok0, ntok;       // query tokens (token = row * Tq + i)
@@ -861,14 +865,14 @@ bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes) {
   const long long least = (a->fixed_p > a->fixed_s ? a->fixed_p : a->fixed_s) + 1;
   const long long share = ceil_div(cost, a->ctas) > least ? ceil_div(cost, a->ctas) : least;
   a->most_pieces = (int)(kt_p / share + kt_s / share + 2);
-  auto align = [](size_t b) { return (b + 255) & ~size_t(255); };
+  auto align = [](size_t b) { return (b + kWsAlign - 1) & ~(kWsAlign - 1); };
   const size_t rows_p = units_p > 0 ? (size_t)(units_p + a->ctas) * (a->box_p * R) : 0;  // a slot per unit and CTA
   const size_t rows_s = units_s > 0 ? (size_t)(units_s + a->ctas) * (a->box_s * R) : 0;
   a->off_os = rows_p * kD * 4;
   a->off_lp = a->off_os + rows_s * kD * 4;
   a->off_ls = a->off_lp + align(rows_p * 4);
   a->off_pieces = a->off_ls + align(rows_s * 4);
-  *bytes = a->off_pieces + align((size_t)(units_p + units_s) * 8);
+  *bytes = a->off_pieces + align((size_t)(units_p + units_s) * 8) + kWsAlign - 16;
   return true;
 }
 
@@ -876,7 +880,7 @@ bool launch_prefix_attn(const PrefixAttnArgs& args, const void* q, long long ldq
                         long long ldp, long long lsp, const void* ks, const void* vs, long long lds, long long lss,
                         void* workspace, cudaStream_t st) {
   PrefixAttnArgs a = args;
-  char* ws = static_cast<char*>(workspace);
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + kWsAlign - 1) & ~uintptr_t(kWsAlign - 1));
   a.part_op = reinterpret_cast<float*>(ws);
   a.part_os = reinterpret_cast<float*>(ws + a.off_os);
   a.part_lp = reinterpret_cast<float*>(ws + a.off_lp);

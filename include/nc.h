@@ -401,8 +401,8 @@ int nc_qk_norm_rope_backward(const void* q, long long ldq, const void* k, long l
  * The sums over keys run in fp32; the weights enter P V in bf16, as in
  * nc_attention.  Requires D == 128, H % H_kv == 0, H / H_kv <= 128, B % G == 0,
  * P_max + S_max <= 2^30, strides at least the width they span (NC_ERR_SHAPE);
- * 16-byte aligned pointers, strides multiples of 8 elements (NC_ERR_ALIGN);
- * softmax_scale > 0 and finite (NC_ERR_ARG); a workspace of
+ * 16-byte aligned pointers (the workspace too), strides multiples of 8 elements
+ * (NC_ERR_ALIGN); softmax_scale > 0 and finite (NC_ERR_ARG); a workspace of
  * nc_prefix_attention_workspace_bytes (0 on invalid sizes), NC_ERR_WORKSPACE
  * otherwise.  Lengths must not change while the call runs. */
 size_t nc_prefix_attention_workspace_bytes(int B, int G, int Tq, int H, int Hkv, int P_max, int S_max, int window);
