@@ -6,7 +6,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
-#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cmath>
@@ -117,8 +117,10 @@ int as_index(PyObject* o) {
 }
 
 // The call's stream (a torch.cuda.Stream, or None for the current one) and its
-// scratch: the caller's tensor, or a new one that lives as long as the stream
-// needs it.
+// scratch: the caller's tensor, or a new one.  The new one comes from the call's
+// stream's own pool: a block of the current stream's may have been freed while
+// that stream still has work queued on it, which the call's stream does not wait
+// for.
 struct Launch {
   void* stream;
   void* workspace = nullptr;
@@ -140,12 +142,9 @@ struct Launch {
   void scratch(const Operands& op, PyObject* o, size_t need) {
     if (o == Py_None) {
       if (need == 0) return;
+      const c10::cuda::CUDAStreamGuard on(
+          c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), (c10::DeviceIndex)op.device));
       own = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)op.device));
-      const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)op.device);
-      if (stream != now.stream())  // it must not be handed out again before that stream is done with it
-        c10::cuda::CUDACachingAllocator::recordStream(
-            own.storage().data_ptr(),
-            c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), (c10::DeviceIndex)op.device));
       workspace = own.data_ptr();
       bytes = need;
       return;
