@@ -9,6 +9,7 @@ build raises immediately; there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -193,6 +194,32 @@ def _stream(stream):
     return C.c_void_p(s.cuda_stream)
 
 
+@contextlib.contextmanager
+def _made_on(stream):
+    """Allocations inside come from the pool of `stream` (None: the current one).  A block of another stream's pool may
+    have been freed while that stream still has work queued on it, which a call on `stream` does not wait for."""
+    import torch
+    if stream is None:
+        yield
+        return
+    if not isinstance(stream, torch.cuda.Stream):  # anything else that has a handle
+        handle = stream.cuda_stream
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        yield
+
+
+def _outputs(device, stream, *shapes_types):
+    """New tensors that a call on `stream` writes and the current stream may read."""
+    import torch
+    with _made_on(stream):
+        made = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in shapes_types]
+    if stream is not None:
+        for t in made:
+            t.record_stream(torch.cuda.current_stream(device))
+    return made
+
+
 # --------------------------------------------------------------------------
 # the C calls, same names
 # --------------------------------------------------------------------------
@@ -295,8 +322,9 @@ def nc_routing_attention(q2, k2, v2, q1, k1, out, window: int, gate_logit: float
     Hkv = k2.shape[2]
     scale = D ** -0.5 if softmax_scale is None else softmax_scale
     if workspace is None:
-        workspace = torch.empty(int(lib().nc_routing_attention_workspace_bytes(B, T, H, D)), dtype=torch.uint8,
-                                device=q2.device)
+        with _made_on(stream):
+            workspace = torch.empty(int(lib().nc_routing_attention_workspace_bytes(B, T, H, D)), dtype=torch.uint8,
+                                    device=q2.device)
     nbytes = workspace.numel() * workspace.element_size()
     _check(lib().nc_routing_attention(_ptr(q2), _ptr(k2), _ptr(v2), _ptr(q1), _ptr(k1), _ptr(out), B, T, H, Hkv, D,
                                       window, gate_logit, scale, _ptr(workspace), nbytes, _stream(stream)),
@@ -337,8 +365,9 @@ def nc_prefix_ce(x, w_u, targets, out_loss, vocab: int, widths, eps: float = 1e-
     V_pad = w_u.shape[0]
     wd, k = _widths(widths)
     if workspace is None:
-        workspace = torch.empty(int(lib().nc_prefix_ce_workspace_bytes(M, Cw, V_pad)), dtype=torch.uint8,
-                                device=x.device)
+        with _made_on(stream):
+            workspace = torch.empty(int(lib().nc_prefix_ce_workspace_bytes(M, Cw, V_pad)), dtype=torch.uint8,
+                                    device=x.device)
     nbytes = workspace.numel() * workspace.element_size()
     _check(lib().nc_prefix_ce(_ptr(x), _ptr(w_u), _ptr(targets), _ptr(out_loss), M, Cw, vocab, V_pad, wd, k, eps,
                               cap, _ptr(workspace), nbytes, _stream(stream)), "nc_prefix_ce")
@@ -473,9 +502,8 @@ class NcModel:
     def forward(self, tokens, targets, want_logits: bool = False, stream=None):
         import torch
         B, T = tokens.shape
-        loss = torch.empty(B * T, dtype=torch.float32, device=self.device)
-        logits = (torch.empty(B * T, self.cfg.vocab, dtype=torch.float32, device=self.device)
-                  if want_logits else None)
+        loss, = _outputs(self.device, stream, (B * T, torch.float32))
+        logits, = _outputs(self.device, stream, ((B * T, self.cfg.vocab), torch.float32)) if want_logits else (None,)
         nc_forward(self.params, tokens, targets, loss, logits, stream)
         return loss, logits
 
@@ -483,7 +511,6 @@ class NcModel:
         """One generation step: (next tokens [B] int32, last-position logits [B, V])."""
         import torch
         B = tokens.shape[0]
-        nxt = torch.empty(B, dtype=torch.int32, device=self.device)
-        logits = torch.empty(B, self.cfg.vocab, dtype=torch.float32, device=self.device)
+        nxt, logits = _outputs(self.device, stream, (B, torch.int32), ((B, self.cfg.vocab), torch.float32))
         nc_generate_next(self.params, tokens, temperature, top_k, uniforms, nxt, logits, stream)
         return nxt, logits

@@ -3,6 +3,7 @@ one that the binding makes."""
 import pytest
 
 from decoder_only_transformer_fwd_b200 import nc
+from nc_cases import make_case
 
 pytestmark = pytest.mark.gpu
 D = 128
@@ -148,3 +149,44 @@ def test_scratch_is_made_on_the_stream_that_is_asked_for(which):
         assert torch.cuda.current_stream() == current
     torch.cuda.synchronize()
     assert nc.nc_get_status()[0] == 0 and torch.equal(got, want)
+
+
+def test_other_calls_on_a_side_stream_leave_the_current_stream_alone():
+    """The same for what nc_routing_attention, nc_prefix_ce and NcModel allocate."""
+    import torch
+    current, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def check(call, nbytes):
+        want = [x.clone() for x in call(None)]
+        seen = _queued_reader_of_a_freed_block(current, nbytes)
+        with torch.cuda.stream(current):
+            got = call(side)
+        torch.cuda.synchronize()
+        assert bool((seen == 7).all()) and all(torch.equal(a, b) for a, b in zip(got, want))
+        assert nc.nc_get_status()[0] == 0
+
+    B, T, H, M = 2, 200, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(10)
+    bf = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()
+    r = [bf(B, T, H, D) for _ in range(5)]
+    out = torch.empty_like(r[0])
+
+    def routing(stream):
+        nc.nc_routing_attention(*r, out, 64, 0.3, stream=stream)
+        return [out]
+
+    check(routing, int(nc.lib().nc_routing_attention_workspace_bytes(B, T, H, D)))
+    x, w_u = torch.randn(M, 768, device="cuda", generator=g), 0.05 * bf(256, 768)
+    y = torch.randint(0, 250, (M,), device="cuda", generator=g).int()
+    loss = torch.empty(2, M, device="cuda")
+
+    def prefix_ce(stream):
+        nc.nc_prefix_ce(x, w_u, y, loss, 250, [256, 512], stream=stream)
+        return [loss]
+
+    check(prefix_ce, int(nc.lib().nc_prefix_ce_workspace_bytes(M, 768, 256)))
+    cfg, _, p, tok, tgt = make_case(1, 2, 48, 48, "fp32", 78)
+    model = nc.NcModel(cfg, p, tok.size)
+    tt, yy, u = torch.from_numpy(tok).cuda(), torch.from_numpy(tgt).cuda(), torch.rand(2, device="cuda", generator=g)
+    check(lambda s: [model.forward(tt, yy, stream=s)[0]], 4 * tok.size)
+    check(lambda s: list(model.generate_next(tt, u, stream=s)), 4 * 2 * cfg.vocab)
