@@ -85,10 +85,15 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   return v;
 }
 
-// e^d - d - 1 without cancellation: its series where the terms fall fast
-// (|d| <= 1/2: the first one left out is 2^-28 of the sum), else from expm1
-__device__ __forceinline__ float exp_excess(float d) {
-  if (fabsf(d) > 0.5f) return expm1f(d) - d;
+// The KL term e^d - d - 1 and its slope e^d - 1, neither with cancellation: the
+// term's series where its terms fall fast (|d| <= 1/2: the first one left out is
+// 2^-28 of the sum), else from expm1, which is then the slope (a term of 2^30
+// would swallow its -1).
+__device__ __forceinline__ float exp_excess(float d, float* slope) {
+  if (fabsf(d) > 0.5f) {
+    *slope = expm1f(d);
+    return *slope - d;
+  }
   float s = 1.0f / 3628800;
   s = fmaf(s, d, 1.0f / 362880);
   s = fmaf(s, d, 1.0f / 40320);
@@ -98,7 +103,9 @@ __device__ __forceinline__ float exp_excess(float d) {
   s = fmaf(s, d, 1.0f / 24);
   s = fmaf(s, d, 1.0f / 6);
   s = fmaf(s, d, 0.5f);
-  return s * d * d;
+  s = s * d * d;
+  *slope = s + d;
+  return s;
 }
 
 // log of a sum S >= 1 in fp64, from a table in shared memory (Tang's method:
@@ -138,7 +145,7 @@ struct RowStats {  // the last three weighted
 // with the borders).
 struct Terms {
   double lp, A, w;
-  float r, d, kl;
+  float r, kl;
   bool cut;
   __device__ __forceinline__ Row begin(const PolicyArgs& a, float zy, float m, double S, const double2* tab, float adv,
                                        float old, float ref, double weight) {
@@ -150,11 +157,11 @@ struct Terms {
     // with the branch decided, fp32 does: the exponents are differences
     r = expf((float)x);
     float slope = cut ? 0.f : -r * adv;
-    kl = d = 0.f;
+    kl = 0.f;
     if (a.ref_logp != nullptr) {
-      d = (float)((double)ref - lp);
-      kl = exp_excess(d);
-      slope -= a.kl_beta * (kl + d);
+      float rise;
+      kl = exp_excess((float)((double)ref - lp), &rise);
+      slope -= a.kl_beta * rise;
     }
     Row t;
     t.gz = (float)w * slope;
