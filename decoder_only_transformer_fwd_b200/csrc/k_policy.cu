@@ -156,12 +156,13 @@ struct Terms {
     cut = (A > 0.0 && x > a.log_high) || (A < 0.0 && x < a.log_low);
     // with the branch decided, fp32 does: the exponents are differences
     r = expf((float)x);
-    float slope = cut ? 0.f : -r * adv;
+    // a term of weight 0 has no part in the gradient, however large it is (0 x inf)
+    float slope = cut || adv == 0.f ? 0.f : -r * adv;
     kl = 0.f;
     if (a.ref_logp != nullptr) {
       float rise;
       kl = exp_excess((float)((double)ref - lp), &rise);
-      slope -= a.kl_beta * rise;
+      if (a.kl_beta > 0.f) slope -= a.kl_beta * rise;
     }
     Row t;
     t.gz = (float)w * slope;
@@ -171,7 +172,8 @@ struct Terms {
   __device__ __forceinline__ RowStats finish(const PolicyArgs& a) const {
     RowStats t;
     t.lp = lp;
-    t.loss = w * (-(cut ? (A > 0.0 ? a.ratio_high : a.ratio_low) : (double)r) * A + (double)a.kl_beta * (double)kl);
+    const double gain = A == 0.0 ? (lp != lp ? lp : 0.0) : (cut ? (A > 0.0 ? a.ratio_high : a.ratio_low) : (double)r) * A;
+    t.loss = w * ((a.kl_beta > 0.f ? (double)a.kl_beta * (double)kl : 0.0) - gain);
     t.kl = w * (double)kl;
     t.clipped = cut ? w : 0.0;
     return t;

@@ -52,3 +52,32 @@ def test_a_reference_that_gives_the_token_almost_no_probability(V, dtype):
             assert abs(stats[1] - kl) <= 2.0 ** -16 * want["size"].sum() + (2.0 ** -22 + 2.0 ** -24) * kl
             assert abs(stats[0] - want["stats"][0]) <= 2.0 ** -16 * want["size"].sum() + (2.0 ** -22 + 2.0 ** -24) * 0.25 * kl
         assert stats[2] == 0
+
+
+@pytest.mark.parametrize("V,dtype", FORMS)
+def test_a_term_of_weight_zero_is_left_out_however_large(V, dtype):
+    """No KL weight and a token that the reference finds e^100 times as likely (the KL statistic alone passes fp32);
+    no advantage and a ratio beyond fp32's and fp64's range, or of an old policy that could not draw the token."""
+    z, y, _ = _logits(V + 1, 6, V, dtype)
+    np.put_along_axis(z[0, :3], y[0, :3, None], -100.0, -1)
+    lp = PL.log_probs(z, y)[0]
+    ref = np.where(np.arange(6) < 3, -5.0, lp - 0.3).astype(np.float32)
+    adv = np.array([[0.7, -0.7, 0.0, 0.0, 0.0, 0.0]], np.float32)
+    old = (lp - np.array([[0.05, 0.05, 0.05, 100.0, 1000.0, np.inf]])).astype(np.float32)
+    stats, logp, dz = _run(z, y, adv, old, ref, dtype, 0.2, 0.28, 0.0, 0)
+    want = PL.policy_loss(z, y, adv, np.where(adv == 0, lp, old), ref, LOW, HIGH, 0.0, 0)
+    _gradient_close(dz, want, dtype)
+    assert np.all(dz[0, 2:] == 0) and stats[1] == np.inf and stats[2] == 0
+    assert abs(stats[0] - want["stats"][0]) <= 2.0 ** -16 * np.abs(want["slope"]).sum() + 2.0 ** -24 * abs(want["stats"][0])
+    # no KL term at all gives the same loss and gradient
+    stats2, _, dz2 = _run(z, y, adv, old, None, dtype, 0.2, 0.28, 0.0, 0)
+    assert stats2[0] == stats[0] and np.array_equal(dz2, dz) and stats2[1] == 0
+
+
+@pytest.mark.parametrize("V", [300, 4099, 9001])
+def test_logits_that_are_not_numbers_show_in_the_loss_without_an_advantage(V):
+    z, y, lp = _logits(V + 2, 3, V, "fp32")
+    z[0, 1, 5] = np.nan
+    stats, logp, dz = _run(z, y, np.zeros((1, 3), np.float32), lp.astype(np.float32), None, "fp32", 0.2, 0.28, 0.0, 0)
+    assert np.isnan(stats[0]) and np.isnan(logp[0, 1]) and np.isnan(dz[0, 1]).all()
+    assert np.isfinite(logp[0, ::2]).all() and np.all(dz[0, ::2] == 0)
