@@ -435,8 +435,9 @@ int nc_prefix_attention(const void* q, long long ldq, const void* k_prefix, cons
  *     from V on are neither read nor written.
  * Row sums and statistics are accumulated in fp32 per thread and fp64 across
  * threads, in a fixed order.  A target outside [-1, V) sets NC_ERR_DATA and
- * counts as -1.  -inf logits have probability 0.  NC_ERR_ARG: a missing
- * pointer, clip_low outside [0, 1), clip_high < 0, kl_beta < 0, norm not 0 or 1;
+ * counts as -1.  -inf logits have probability 0.  A term of weight 0 (A or
+ * kl_beta) is left out, however large.  NC_ERR_ARG: a missing pointer,
+ * clip_low outside [0, 1), clip_high < 0, kl_beta < 0, norm not 0 or 1;
  * NC_ERR_SHAPE: B, T or V < 1, B T or V above 2^30, a stride below V;
  * NC_ERR_ALIGN: rows not aligned to their element, workspace not to 16 bytes;
  * NC_ERR_WORKSPACE. */

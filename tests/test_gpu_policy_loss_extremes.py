@@ -81,3 +81,24 @@ def test_logits_that_are_not_numbers_show_in_the_loss_without_an_advantage(V):
     stats, logp, dz = _run(z, y, np.zeros((1, 3), np.float32), lp.astype(np.float32), None, "fp32", 0.2, 0.28, 0.0, 0)
     assert np.isnan(stats[0]) and np.isnan(logp[0, 1]) and np.isnan(dz[0, 1]).all()
     assert np.isfinite(logp[0, ::2]).all() and np.all(dz[0, ::2] == 0)
+
+
+@pytest.mark.parametrize("norm", [0, 1])
+@pytest.mark.parametrize("V,dtype", FORMS)
+def test_exponentials_beyond_fp32_whose_weighted_terms_fit(V, dtype, norm):
+    """Ratios and KL terms of e^90 = 1.2e39: with the weight (1/8 here), the advantage and kl_beta they fit fp32 again.
+    The statistic of the KL term has the weight alone, its error follows lp's (2^-17 + 2^-24 |lp| in the exponent)."""
+    T, beta = 8, 0.02
+    z, y, _ = _logits(V + 3, T, V, dtype)
+    np.put_along_axis(z[0, 4:6], y[0, 4:6, None], -100.0, -1)
+    lp = PL.log_probs(z, y)[0]
+    d = np.array([[0.1, -0.2, 0.3, 0.0, 90.0, 85.0, -0.1, 0.2]])
+    x = np.array([[90.0, 85.0, 82.0, 90.0, 0.1, -0.1, 0.1, 79.0]])
+    adv = np.array([[-0.1, -1e-30, -0.5, 0.9, 0.5, -0.5, 0.3, -0.1]], np.float32)
+    old, ref = (lp - x).astype(np.float32), (lp + d).astype(np.float32)
+    stats, logp, dz = _run(z, y, adv, old, ref, dtype, 0.2, 0.28, beta, norm)
+    want = PL.policy_loss(z, y, adv, old, ref, LOW, HIGH, beta, norm)
+    assert np.abs(want["dz"]).max() > 1e36 and want["stats"][1] > 1e38
+    _gradient_close(dz, want, dtype)
+    assert abs(stats[0] - want["stats"][0]) <= 2.0 ** -16 * want["size"].sum() + 2.0 ** -24 * abs(want["stats"][0])
+    assert abs(stats[1] - want["stats"][1]) <= 2.0 ** -15 * want["stats"][1] and abs(stats[2] - want["stats"][2]) <= 2.0 ** -24
