@@ -1,5 +1,6 @@
 """Build libnc.so in-tree for sm_100a with nvcc (one object per .cu, then link),
 and _ncpy.so, the native part of the Python binding (csrc/nc_py.cpp), with g++.
+Only the latter needs torch and Python's headers; without them it is left out.
 
     python -m decoder_only_transformer_fwd_b200.build [--force] [--verbose]
 
@@ -46,13 +47,19 @@ def _stale(src, obj, hdr_mtime):
     return os.path.getmtime(src) > t or hdr_mtime > t
 
 
-def build_py(force: bool = False, verbose: bool = False) -> str:
-    """_ncpy.so against torch's headers and libraries (which are loaded by the time it is) and libnc.so beside it."""
+def build_py(force: bool = False, verbose: bool = False) -> str | None:
+    """_ncpy.so against torch's headers and libraries (which are loaded by the time it is) and libnc.so beside it.
+    None where torch or Python's headers are not installed: C users need neither."""
     src = os.path.join(CSRC, "nc_py.cpp")
     newest = max(os.path.getmtime(f) for f in (src, os.path.join(ROOT, "include", "nc.h")))
     if not force and os.path.exists(PYLIB) and os.path.getmtime(PYLIB) > newest:
         return PYLIB
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = importlib.util.find_spec("torch")
+    python_h = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    if torch is None or not os.path.exists(python_h):
+        sys.stderr.write(f"_ncpy.so (Python binding) is not built: no {'torch' if torch is None else python_h}\n")
+        return None
+    torch_dir = torch.submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(NVCC))
     include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
