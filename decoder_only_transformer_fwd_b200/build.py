@@ -50,16 +50,20 @@ def _stale(src, obj, hdr_mtime):
 def build_py(force: bool = False, verbose: bool = False) -> str | None:
     """_ncpy.so against torch's headers and libraries (which are loaded by the time it is) and libnc.so beside it.
     None where torch or Python's headers are not installed: C users need neither."""
-    src = os.path.join(CSRC, "nc_py.cpp")
-    newest = max(os.path.getmtime(f) for f in (src, os.path.join(ROOT, "include", "nc.h")))
-    if not force and os.path.exists(PYLIB) and os.path.getmtime(PYLIB) > newest:
-        return PYLIB
     torch = importlib.util.find_spec("torch")
     python_h = os.path.join(sysconfig.get_paths()["include"], "Python.h")
     if torch is None or not os.path.exists(python_h):
         sys.stderr.write(f"_ncpy.so (Python binding) is not built: no {'torch' if torch is None else python_h}\n")
         return None
     torch_dir = torch.submodule_search_locations[0]
+    with open(os.path.join(torch_dir, "version.py")) as f:  # what it is built for: it loads with no other
+        target = f"{sysconfig.get_config_var('EXT_SUFFIX')}\n{torch_dir}\n{f.read()}"
+    src, built_for = os.path.join(CSRC, "nc_py.cpp"), os.path.join(OBJ, "_ncpy.target")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(ROOT, "include", "nc.h")))
+    if not force and os.path.exists(PYLIB) and os.path.getmtime(PYLIB) > newest and os.path.exists(built_for):
+        with open(built_for) as f:
+            if f.read() == target:
+                return PYLIB
     cuda = os.path.dirname(os.path.dirname(NVCC))
     include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
@@ -69,6 +73,8 @@ def build_py(force: bool = False, verbose: bool = False) -> str | None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed:\n{r.stderr}")
+    with open(built_for, "w") as f:
+        f.write(target)
     if verbose:
         sys.stderr.write(f"[g++] nc_py.cpp\n{r.stderr}")
     return PYLIB
