@@ -11,8 +11,12 @@
 // The prefix keys of a group are read once for all its rows: the queries of
 // all rows (and of all query heads of one key head) form the 128-row tiles of
 // one matrix product, so a long prefix costs its bytes once instead of once
-// per row.  What bounds it: reading the caches from HBM, as long as a key
-// head has fewer than about 250 query rows per group.
+// per row.  What bounds it (one B200): under a long prefix HBM (64 rows, 12
+// heads, 32768 shared and up to 1024 own keys: 69 us, 5.5 TB/s); for few keys the
+// latency of two kernels, tables, one tile and the join (10.5 us); in between a
+// tile's softmax chain, 0.6 us per SM, which a row's own keys pay in full for the
+// one or few queries that they have (16 rows, 2048 + 512 keys, window 1024: 16.6
+// us, its bytes take 3.9).
 //
 // The work of a key head is a sequence of units, prefix units (group, 128-row
 // query tile) and then suffix units (row, query tile), each a run of 64-key
@@ -20,9 +24,8 @@
 // of heads), and the CTAs of a band cut its sequence of tiles into equal shares,
 // as the lengths in memory give them: a long unit is spread over many CTAs, a
 // CTA takes many short ones, all finish together, and the heads' keys of one
-// token, which lie side by side in memory, are read at the same time (64 rows,
-// 12 heads, 32768 keys, attention kernel alone: 46 us with the heads one after
-// the other, 40 us with one head's keys contiguous).
+// token, which lie side by side in memory, are read at the same time (68.8 us in
+// the first case above, 69.4 with the heads one after the other).
 // What a CTA does of a unit is a piece; it leaves its rows' normalised output
 // (fp32) and log-sum-exp in the workspace, at slot (unit + CTA of the band),
 // which no two pieces share.  k_prefix_combine joins a row's pieces with weights
@@ -610,6 +613,9 @@ __global__ void __launch_bounds__(kThreads, 2)
               const float2 e = __ffma2_rn(make_float2(x[32 * hf + 2 * i], x[32 * hf + 2 * i + 1]), c2, mc2);
               const float2 q = make_float2(ex2(e.x), ex2(e.y));
               sm[i & 1] = __fadd2_rn(sm[i & 1], q);
+              // V is bf16, and the product takes operands of one type; the sum keeps
+              // the fp32 weights.  Error of the output against fp64, relative in the
+              // mean: 0.0022, of which its own rounding to bf16 is 0.0016.
               pk[i] = pack_bf16(q.x, q.y);
             }
             ptx::tmem_st16(tS + (uint32_t)(16 * hf), pk);
@@ -861,7 +867,9 @@ bool prefix_attn_plan(PrefixAttnArgs* a, size_t* bytes) {
   a->fixed_s = unit_fixed(a->box_s * R);
   const long long cost = units_p * (kt_p + a->fixed_p) + units_s * (kt_s + a->fixed_s);
   if (cost > most) return false;
-  // pieces that a row may have with full caches
+  // About how many pieces a row has with full caches: an estimate for the choice of
+  // the join alone, which takes any number.  Shorter lengths make the shares smaller
+  // and may cut a row more often than this, or less.
   const long long least = (a->fixed_p > a->fixed_s ? a->fixed_p : a->fixed_s) + 1;
   const long long share = ceil_div(cost, a->ctas) > least ? ceil_div(cost, a->ctas) : least;
   a->most_pieces = (int)(kt_p / share + kt_s / share + 2);
@@ -903,13 +911,16 @@ bool launch_prefix_attn(const PrefixAttnArgs& args, const void* q, long long ldq
   }
   const long long rows = (long long)tokens * a.H;
   LaunchScope scope_(KK_PREFIX_ATTN, st);
-  // A row's pieces are joined by one warp, by four where rows are few or may have
+  // A row's pieces are joined by one warp, by four where rows are few or should have
   // many pieces and 148 SMs hold all rows' CTAs at once, by sixteen where both.
-  // Measured in us for the whole call, (rows, pieces at most), one against four
+  // Measured in us for the whole call, (rows, pieces estimated), one against four
   // warps: (192, 5) 16.2, 15.5; (384, 7) 19.0, 18.5; (512, 6) 13.7, 14.4; (1152, 4)
   // 31.9, 33.2; (768, 9) 69.6, 69.1; (768, 12) 18.4, 18.7; (1280, 20) 29.4, 28.1;
   // (2048, 6) 27.0, 27.7; (3600, 9) 27.8, 32.1.
   // Four against sixteen: (12, 171) 16.1, 13.6; (48, 4) 10.7, 11.4.
+  // Where lengths are far from the caches' the estimate may choose wrongly: 768 rows
+  // over 512 + 64 keys in caches of 32768 + 1024 take four, 18.6 for 17.4; 500 rows
+  // of which one has 12800 keys and the others none take one, 18.2 for 15.0.
   if (rows <= 148 && a.most_pieces > 32) return launch_pdl(k_prefix_combine<16>, dim3((unsigned)rows), dim3(512), 0, st, 1, a) == cudaSuccess;
   if (rows <= 3 * 148 || (a.most_pieces > 8 && rows <= 16 * 148)) return launch_pdl(k_prefix_combine<4>, dim3((unsigned)rows), dim3(128), 0, st, 1, a) == cudaSuccess;
   return launch_pdl(k_prefix_combine<1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, a) == cudaSuccess;

@@ -237,7 +237,7 @@ struct PrefixAttnArgs {
   // filled by prefix_attn_plan(): query tokens per tile and tiles per sequence
   // (prefix, suffix), sequences per bin and bins of the tables of starts
   int band, bands, per_band;  // key heads per band, bands, CTAs per band
-  int most_pieces;         // of a row, with full caches
+  int most_pieces;         // of a row, estimated for full caches
   int fixed_p, fixed_s;    // what a unit costs besides its tiles
   int rows_per_group, ctas, box_p, box_s, tiles_p, tiles_s, bin_p, bin_s, bins_p, bins_s;
   size_t off_os, off_lp, off_ls, off_pieces;
