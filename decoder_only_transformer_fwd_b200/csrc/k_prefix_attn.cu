@@ -13,9 +13,9 @@
 // one matrix product, so a long prefix costs its bytes once instead of once
 // per row.  What bounds it (one B200): under a long prefix HBM (64 rows, 12
 // heads, 32768 shared and up to 1024 own keys: 69 us, 5.5 TB/s); for few keys the
-// latency of two kernels, tables, one tile and the join (10.5 us); in between a
+// latency of two kernels, tables, one tile and the join (10.9 us); in between a
 // tile's softmax chain, 0.6 us per SM, which a row's own keys pay in full for the
-// one or few queries that they have (16 rows, 2048 + 512 keys, window 1024: 16.6
+// one or few queries that they have (16 rows, 2048 + 512 keys, window 1024: 16.3
 // us, its bytes take 3.9).
 //
 // The work of a key head is a sequence of units, prefix units (group, 128-row
