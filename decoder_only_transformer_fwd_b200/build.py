@@ -73,6 +73,7 @@ def build_py(force: bool = False, verbose: bool = False) -> str | None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed:\n{r.stderr}")
+    os.makedirs(OBJ, exist_ok=True)
     with open(built_for, "w") as f:
         f.write(target)
     if verbose:
